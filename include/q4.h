@@ -1,6 +1,8 @@
 /*
  * q4.h -- C ABI of the weight-only 4-bit codebook linear layer for NVIDIA
- * B200 (sm_100a), with a two-bit variant (q4_pack2, q4_dequant2, q4_gemv2).
+ * B200 (sm_100a), with a two-bit variant (q4_pack2, q4_dequant2, q4_gemv2)
+ * and the microscaled 4-bit format with expert-routed layers (q4_pack_mx to
+ * q4_combine_grad, below).
  *
  * The operation.  A linear layer y = x * W^T whose weight matrix W [N][K]
  * (N outputs, K inputs) is stored as 4-bit codes into a 16-entry binary16
@@ -78,8 +80,12 @@ typedef enum {
     Q4_ERR_ALIGN = 3,
     Q4_ERR_ARCH = 4,
     Q4_ERR_CUDA = 5,
-    Q4_ERR_TOO_LARGE = 6  /* q4_gemm_noalloc only: x does not fit its fixed scratch */
+    Q4_ERR_TOO_LARGE = 6  /* the work does not fit the scratch it is given (q4_gemm_noalloc, q4_gemm_mx,
+                             q4_gemm_experts, q4_ring_gemm) */
 } q4_status;
+
+/* Element types of the calls that take one (float arrays of either side). */
+typedef enum { Q4_F32 = 0, Q4_BF16 = 1, Q4_F16 = 2 } q4_type;
 
 #define Q4_ABI_VERSION 1
 #define Q4_GROUP 64
@@ -316,6 +322,124 @@ q4_status q4_gemv2(const uint8_t* codes, const uint16_t* scales,
                    int64_t N, int64_t K, q4_stream_t stream);
 
 /*
+ * The microscaled 4-bit format: groups of 32 weights along K, e2m1 codes
+ * (sign, two exponent bits, one mantissa bit: 0, 0.5, 1, 1.5, 2, 3, 4, 6) and
+ * one power-of-two scale, an e8m0 exponent byte (255 stands for NaN):
+ *     W[n][k] = e2m1(code(n, k)) * 2^(byte(n, k / 32) - 127)
+ * Source: the "cuda-oxide" abstract (an MXFP4 decoder on FP4 block-scaled
+ * matrix instructions); element and scale formats are those of the OCP
+ * Microscaling Formats specification.
+ * Storage is in blocks of 128 rows x 128 k, Nb = ceil(N / 128) by
+ * Kb = ceil(K / 128), padded with zeros:
+ *   codes   uint8_t [Nb][Kb][128][64]  row r of a block: k = 2 j in the low,
+ *                                      2 j + 1 in the high nibble of byte j
+ *   scales  uint8_t [Nb][Kb][512]      row r, group g of a block at
+ *                                      (r % 32) * 16 + (r / 32) * 4 + g
+ * A stack of E matrices (experts) is E of these in a row.  N >= 0, 1 <= K <=
+ * Q4_MAX_K, any values (no multiple is asked for), and E * Nb * Kb at most
+ * Q4_MX_MAX_BLOCKS; arrays of other types are row-major and contiguous.
+ *
+ * q4_pack_mx -- quantise w [E][N][K] of type w_type.  Per group, with a the
+ * largest magnitude: byte = floor(log2 a) - 2 + 127, at least 0 (0 where a is
+ * 0); code = w * 2^(127 - byte) rounded to the nearest e2m1 value, ties to
+ * the even code, saturating at 6.  A group that holds an infinity or NaN gets
+ * byte 255.  Bit-identical to a serial IEEE implementation of these steps.
+ * q4_dequant_mx -- write W [E][N][K] in w_type: exact in binary32 and
+ * bfloat16 (infinite where 6 * 2^127 leaves the range), rounded once in
+ * binary16.
+ * Validation of both: Q4_ERR_SHAPE (also for a bad type), Q4_ERR_NULL,
+ * Q4_ERR_ALIGN (16 bytes), Q4_ERR_ARCH, Q4_ERR_CUDA; E == 0 or N == 0 is
+ * valid and launches nothing.
+ */
+#define Q4_MX_MAX_BLOCKS 16777215LL
+q4_status q4_pack_mx(const void* w, q4_type w_type, uint8_t* codes, uint8_t* scales,
+                     int64_t E, int64_t N, int64_t K, q4_stream_t stream);
+q4_status q4_dequant_mx(const uint8_t* codes, const uint8_t* scales, void* w_out,
+                        q4_type w_type, int64_t E, int64_t N, int64_t K, q4_stream_t stream);
+
+/*
+ * q4_gemm_mx -- y[m][n] = sum_k W[n][k] x[m][k] for any M >= 0, W microscaled,
+ * x bfloat16, y binary32 (Q4_F32) or bfloat16 (Q4_BF16, one rounding), fully
+ * overwritten.  Runs on the block-scaled tensor-core instructions, which take
+ * codes and exponents as stored; x is split into two 8-bit parts whose sum is
+ * x to within 2^-22 of the largest |x| of each 32 (exactly, wherever |x| is
+ * at least 2^-14 of it), products are exact and sums binary32.  Within 1e-4 * sum_k |W x| + 1e-6 of the exact sum, and for
+ * a given device and shape the same bits on every run.  Input domain: x
+ * finite; a row of x that holds an infinity or NaN gives a row of NaN.
+ *
+ * q4_gemm_experts -- the same for rows grouped by expert, W a stack of E
+ * matrices: y[p][n] = sum_k W[e][n][k] x[rows[p]][k] for offsets[e] <= p <
+ * offsets[e + 1], p < T.  offsets [E + 1] starts at 0 and does not decrease
+ * (values out of order are clamped); rows of y at and past offsets[E] are set
+ * to zero.  rows == NULL takes row p of x itself; a row index outside
+ * [0, Mx) gives a row of zeros.  offsets and rows are read on the device, so
+ * the call neither copies nor synchronizes; experts without rows cost
+ * nothing.  E <= Q4_MAX_EXPERTS.
+ *
+ * Both use the caller's workspace (16-byte aligned, any contents, q4_gemm_mx_
+ * workspace / q4_gemm_experts_workspace bytes; -1 for bad sizes) for x's parts
+ * and partial sums.  It must not be used by anything else until the call has
+ * run on the stream: calls that may overlap, recorded graphs among them, need
+ * workspaces of their own.  Two launches a call.
+ * Validation: Q4_ERR_SHAPE (M, T, Mx above 2^30 included), Q4_ERR_NULL,
+ * Q4_ERR_ALIGN (codes 32 bytes, all else 16), Q4_ERR_TOO_LARGE (workspace too
+ * small), Q4_ERR_ARCH, Q4_ERR_CUDA.  M, T or N of 0 is valid: nothing runs.
+ */
+#define Q4_MAX_EXPERTS 1024
+int64_t q4_gemm_mx_workspace(int64_t M, int64_t N, int64_t K);
+q4_status q4_gemm_mx(const uint8_t* codes, const uint8_t* scales, const uint16_t* x, void* y,
+                     q4_type y_type, int64_t M, int64_t N, int64_t K, void* workspace,
+                     int64_t workspace_bytes, q4_stream_t stream);
+int64_t q4_gemm_experts_workspace(int64_t T, int64_t E, int64_t N, int64_t K);
+q4_status q4_gemm_experts(const uint8_t* codes, const uint8_t* scales, const uint16_t* x,
+                          const int32_t* rows, const int32_t* offsets, void* y, q4_type y_type,
+                          int64_t Mx, int64_t T, int64_t E, int64_t N, int64_t K,
+                          void* workspace, int64_t workspace_bytes, q4_stream_t stream);
+
+/*
+ * Tokens sorted by expert and back, for a batch of M tokens with `top` choices
+ * each, T = M * top.
+ * Source: the "Trapetum" overview ("Frontier models on your own hardware":
+ * a mixture-of-experts model decoded from packed experts).
+ *
+ * q4_sort_experts -- stable order of the choices by expert.  ids [M][top] are
+ * expert numbers, int32 or (wide != 0) int64; ids outside [0, E), of padded
+ * tokens for instance, drop their choice.  Writes offsets [E + 1] (first
+ * position of each expert; offsets[E] = choices kept), rows [T] (token of
+ * each position, -1 at and past offsets[E]) and places [M][top] (position of
+ * each choice; -1 - position, with positions from offsets[E] on, for dropped
+ * ones).  Choices of one expert keep their order.
+ *
+ * q4_dispatch -- xs [T][K] = row of each position's token of x [M][K], zeros
+ * for dropped choices.  Its gradient is q4_combine without weights.
+ *
+ * q4_combine -- out[m] = sum_j weights[m][j] * ys[places[m][j]] over the kept
+ * choices, in order of j, in binary32, rounded once to `type`.  weights
+ * binary32 [M][top], or NULL for ones.  Without weights its gradient is
+ * q4_dispatch.
+ *
+ * q4_combine_grad -- the gradients of q4_combine: dys[places[m][j]] =
+ * weights[m][j] * dout[m], zeros at dropped choices' positions, and
+ * dweights[m][j] = sum_k dout[m][k] ys[places[m][j]][k], 0 for dropped ones.
+ *
+ * places come from q4_sort_experts or obey its rules: no position twice;
+ * positions past T are skipped.  x, xs, ys, out, dout and dys have `type`.
+ * Validation: Q4_ERR_SHAPE (a negative size, K < 1, K > Q4_MAX_K, top < 1,
+ * T > 2^31 - 1, E outside 1 .. Q4_MAX_EXPERTS, a bad type), Q4_ERR_NULL, Q4_ERR_ALIGN
+ * (16 bytes), Q4_ERR_ARCH, Q4_ERR_CUDA.  M == 0 is valid: q4_sort_experts then
+ * sets offsets to zero, the others do nothing.
+ */
+q4_status q4_sort_experts(const void* ids, int wide, int32_t* offsets, int32_t* rows,
+                          int32_t* places, int64_t M, int64_t top, int64_t E, q4_stream_t stream);
+q4_status q4_dispatch(const void* x, const int32_t* places, void* xs, q4_type type, int64_t M,
+                      int64_t top, int64_t K, q4_stream_t stream);
+q4_status q4_combine(const void* ys, const int32_t* places, const float* weights, void* out,
+                     q4_type type, int64_t M, int64_t top, int64_t K, q4_stream_t stream);
+q4_status q4_combine_grad(const void* dout, const void* ys, const int32_t* places,
+                          const float* weights, void* dys, float* dweights, q4_type type,
+                          int64_t M, int64_t top, int64_t K, q4_stream_t stream);
+
+/*
  * Decode steps as one CUDA graph.
  * Source: "deep-fold", "Method" table (the decode runs a full greedy step as
  * one CUDA graph); "Trapetum" landing page (the 7B decode rate it reports
@@ -387,7 +511,8 @@ q4_status q4_wait_selftest(uint32_t limit_us, int arrive, uint32_t* waited_us);
  * set by failed checks since the last call and clear them: bit 0 the M <= 4
  * decode kernel, 1 the M = 2..24 kernel, 2 the tensor-core GEMM, 3 the
  * fallback small-M kernel, 4 pack / dequant / embedding rows, 5 the two-bit
- * kernels.  Always 0 in a release build.  Returns Q4_ERR_NULL for a NULL
+ * kernels, 6 microscaled pack / dequant, 7 the microscaled products, 8 the
+ * expert sort and row movement.  Always 0 in a release build.  Returns Q4_ERR_NULL for a NULL
  * flags, Q4_ERR_CUDA if a CUDA call fails.
  *
  * q4_bounds_checked -- 1 if this library was built with the checks, else 0.
@@ -401,7 +526,7 @@ int q4_bounds_checked(void);
  * a device word, the kernel drains what it has in flight, frees its tensor
  * memory and exits, leaving its output incomplete.  This call synchronizes the
  * current device, stores the bits set since the last call in *flags and
- * clears them: bits 1-3 the two-bit GEMV (producer, drain and consumer
+ * clears them: bit 0 the microscaled products, bits 1-3 the two-bit GEMV (producer, drain and consumer
  * waits), bits 4-11 the M = 1 GEMV (bit 7: q4_wait_selftest's wait ran out;
  * bit 8: its shared-memory layout did not match the device; bits 9-11:
  * producer, drain and consumer waits), bits

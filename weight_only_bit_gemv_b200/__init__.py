@@ -17,6 +17,13 @@ Tensor conventions (all contiguous, on one CUDA device):
   scales   float16 or uint16  [N, K/64]  (binary16 bits)
   x        bfloat16 or uint16 [M, K]     (bfloat16 bits)
   y        float32            [M, N]
+
+The microscaled 4-bit calls (q4_pack_mx and the products on it) take blocks of
+128 rows x 128 k, padded with zeros, Nb = ceil(N / 128), Kb = ceil(K / 128):
+  codes    uint8              [Nb, Kb, 128, 64]   a stack of experts: [E, Nb, Kb, 128, 64]
+  scales   uint8              [Nb, Kb, 512]                          [E, Nb, Kb, 512]
+They run on the tensors' device whatever the current device is, and what they
+allocate belongs to the stream that they run on.
 """
 from __future__ import annotations
 
@@ -113,6 +120,22 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
     lib.q4_step_destroy.restype = ctypes.c_int
     lib.q4_wait_selftest.argtypes = [ctypes.c_uint32, ctypes.c_int, ctypes.POINTER(ctypes.c_uint32)]
     lib.q4_wait_selftest.restype = ctypes.c_int
+    T, W = ctypes.c_int, ctypes.c_int
+    lib.q4_pack_mx.argtypes = [P, T, P, P, I64, I64, I64, S]
+    lib.q4_dequant_mx.argtypes = [P, P, P, T, I64, I64, I64, S]
+    lib.q4_gemm_mx.argtypes = [P, P, P, P, T, I64, I64, I64, P, I64, S]
+    lib.q4_gemm_experts.argtypes = [P, P, P, P, P, P, T, I64, I64, I64, I64, I64, P, I64, S]
+    lib.q4_sort_experts.argtypes = [P, W, P, P, P, I64, I64, I64, S]
+    lib.q4_dispatch.argtypes = [P, P, P, T, I64, I64, I64, S]
+    lib.q4_combine.argtypes = [P, P, P, P, T, I64, I64, I64, S]
+    lib.q4_combine_grad.argtypes = [P, P, P, P, P, P, T, I64, I64, I64, S]
+    for f in ("q4_pack_mx", "q4_dequant_mx", "q4_gemm_mx", "q4_gemm_experts", "q4_sort_experts",
+              "q4_dispatch", "q4_combine", "q4_combine_grad"):
+        getattr(lib, f).restype = ctypes.c_int
+    lib.q4_gemm_mx_workspace.argtypes = [I64, I64, I64]
+    lib.q4_gemm_mx_workspace.restype = I64
+    lib.q4_gemm_experts_workspace.argtypes = [I64, I64, I64, I64]
+    lib.q4_gemm_experts_workspace.restype = I64
     lib.q4_bounds_flags.argtypes = [ctypes.POINTER(ctypes.c_uint32)]
     lib.q4_bounds_flags.restype = ctypes.c_int
     lib.q4_bounds_checked.argtypes = []
@@ -324,6 +347,322 @@ def q4_gemm_noalloc(codes, scales, codebook, x, y, stream=None) -> torch.Tensor:
     if y is None:
         raise ValueError("q4_gemm_noalloc writes into a caller-provided y")
     return _matmul("q4_gemm_noalloc", codes, scales, codebook, x, y, stream)
+
+
+# ---- microscaled 4-bit matrices and layers routed by expert -----------------
+
+MX_BLOCK = 128
+MX_GROUP = 32
+_TYPE = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+
+
+class _On:
+    """The device, stream and allocations of one call: the tensors' device is
+    made current, and what the call allocates belongs to the stream that it
+    runs on, so that it can be freed before the call has run."""
+
+    __slots__ = ("device", "stream", "_guards")
+
+    def __init__(self, t: torch.Tensor, stream):
+        self.device = t.device
+        index = t.device.index
+        self._guards = ()
+        if stream is None:
+            self.stream = torch._C._cuda_getCurrentRawStream(index)
+            if index != torch.cuda.current_device():
+                self._guards = (torch.cuda.device(index),)
+        else:
+            self.stream = int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
+            owner = stream if hasattr(stream, "cuda_stream") else \
+                torch.cuda.ExternalStream(self.stream, device=t.device)
+            self._guards = (torch.cuda.device(index), torch.cuda.stream(owner))
+
+    def __enter__(self):
+        for g in self._guards:
+            g.__enter__()
+        return self
+
+    def __exit__(self, *exc):
+        for g in reversed(self._guards):
+            g.__exit__(*exc)
+
+    def empty(self, shape, dtype) -> torch.Tensor:
+        return torch.empty(shape, dtype=dtype, device=self.device)
+
+
+def _operand(t, name: str, dtypes, shape, on: torch.Tensor) -> None:
+    """One tensor of a call: its type, shape, layout and device."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: dtype {t.dtype} not in {dtypes}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)} != {tuple(shape)}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.device != on.device:
+        raise ValueError(f"{name} is on {t.device}, not on {on.device}")
+
+
+def _dims(t, name: str, dims, form: str) -> None:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() not in dims:
+        raise ValueError(f"{name} must be {form}")
+
+
+_BYTES = (torch.uint8,)
+_I32 = (torch.int32,)
+_IDS = (torch.int32, torch.int64)
+_F32 = (torch.float32,)
+_FLOATS = tuple(_TYPE)
+_OUT = (torch.float32, torch.bfloat16)
+
+
+def _type(dtype, allowed, name: str) -> int:
+    if dtype not in allowed:
+        raise TypeError(f"{name}: dtype {dtype} not in {allowed}")
+    return _TYPE[dtype]
+
+
+def _mx_sizes(codes, scales, N, K):
+    """(E or None, N, K) of a packed matrix or stack, checked against its blocks."""
+    _dims(codes, "codes", (4, 5), "[Nb, Kb, 128, 64] or [E, Nb, Kb, 128, 64]")
+    lead, (nb, kb) = codes.shape[:-4], codes.shape[-4:-2]
+    if codes.shape[-2:] != (MX_BLOCK, MX_BLOCK // 2):
+        raise ValueError("codes must be [..., Nb, Kb, 128, 64]")
+    N = nb * MX_BLOCK if N is None else int(N)
+    K = kb * MX_BLOCK if K is None else int(K)
+    if -(-N // MX_BLOCK) != nb or -(-K // MX_BLOCK) != kb or N < 0:
+        raise ValueError(f"N = {N}, K = {K} do not have {nb} x {kb} blocks of {MX_BLOCK}")
+    _operand(codes, "codes", _BYTES, codes.shape, codes)
+    _operand(scales, "scales", _BYTES, (*lead, nb, kb, 512), codes)
+    return (lead[0] if lead else None), N, K
+
+
+def q4_pack_mx(w: torch.Tensor, codes: torch.Tensor = None, scales: torch.Tensor = None, stream=None):
+    """Quantize w [N, K] or [E, N, K] (float32, bfloat16 or float16) into
+    microscaled 4-bit (codes, scales) blocks; allocates them if not given."""
+    _dims(w, "w", (2, 3), "[N, K] or [E, N, K]")
+    N, K = w.shape[-2:]
+    lead = tuple(w.shape[:-2])
+    nb, kb = -(-N // MX_BLOCK), -(-K // MX_BLOCK)
+    _operand(w, "w", _FLOATS, w.shape, w)
+    with _On(w, stream) as on:
+        if codes is None:
+            codes = on.empty((*lead, nb, kb, MX_BLOCK, MX_BLOCK // 2), torch.uint8)
+        else:
+            _operand(codes, "codes", _BYTES, (*lead, nb, kb, MX_BLOCK, MX_BLOCK // 2), w)
+        if scales is None:
+            scales = on.empty((*lead, nb, kb, 512), torch.uint8)
+        else:
+            _operand(scales, "scales", _BYTES, (*lead, nb, kb, 512), w)
+        st = load().q4_pack_mx(w.data_ptr(), _TYPE[w.dtype], codes.data_ptr(), scales.data_ptr(),
+                               lead[0] if lead else 1, N, K, on.stream)
+    _check(st, "q4_pack_mx")
+    return codes, scales
+
+
+def q4_dequant_mx(codes: torch.Tensor, scales: torch.Tensor, w_out: torch.Tensor = None, N: int = None,
+                  K: int = None, dtype: torch.dtype = torch.float32, stream=None) -> torch.Tensor:
+    """W [N, K] or [E, N, K] from its microscaled blocks, as w_out's type or
+    ``dtype``.  N and K default to whole blocks."""
+    E, N, K = _mx_sizes(codes, scales, N, K)
+    shape = (N, K) if E is None else (E, N, K)
+    with _On(codes, stream) as on:
+        if w_out is None:
+            _type(dtype, _FLOATS, "dtype")
+            w_out = on.empty(shape, dtype)
+        else:
+            _operand(w_out, "w_out", _FLOATS, shape, codes)
+        st = load().q4_dequant_mx(codes.data_ptr(), scales.data_ptr(), w_out.data_ptr(),
+                                  _TYPE[w_out.dtype], 1 if E is None else E, N, K, on.stream)
+    _check(st, "q4_dequant_mx")
+    return w_out
+
+
+def _scratch(on, workspace, need: int, of: torch.Tensor, what: str):
+    """A call's workspace: the caller's, or one of the call's own."""
+    if need < 0:
+        _check(2, what)
+    if workspace is None:
+        return on.empty(need, torch.uint8)
+    _operand(workspace, "workspace", _BYTES, workspace.shape, of)
+    return workspace
+
+
+def q4_gemm_mx_workspace(M: int, N: int, K: int) -> int:
+    """Bytes of workspace that q4_gemm_mx needs (-1 for sizes it refuses)."""
+    return int(load().q4_gemm_mx_workspace(int(M), int(N), int(K)))
+
+
+def q4_gemm_experts_workspace(T: int, E: int, N: int, K: int) -> int:
+    """Bytes of workspace that q4_gemm_experts needs (-1 for sizes it refuses)."""
+    return int(load().q4_gemm_experts_workspace(int(T), int(E), int(N), int(K)))
+
+
+def q4_gemm_mx(codes: torch.Tensor, scales: torch.Tensor, x: torch.Tensor, y: torch.Tensor = None,
+               N: int = None, dtype: torch.dtype = torch.float32, workspace: torch.Tensor = None,
+               stream=None) -> torch.Tensor:
+    """y [M, N] = x [M, K] @ W^T for any M, W a microscaled matrix, x bfloat16,
+    y float32 or bfloat16 (y's type, or ``dtype``).  N defaults to whole
+    blocks.  ``workspace`` (uint8, at least q4_gemm_mx_workspace bytes) is
+    allocated if not given; one that is given must not be shared by calls
+    that may overlap."""
+    _dims(x, "x", (2,), "[M, K]")
+    M, K = x.shape
+    E, N, K = _mx_sizes(codes, scales, N, K)
+    if E is not None:
+        raise ValueError("codes is a stack of matrices: use q4_gemm_experts")
+    _operand(x, "x", _BF16, x.shape, codes)
+    lib = load()
+    with _On(codes, stream) as on:
+        if y is None:
+            _type(dtype, _OUT, "dtype")
+            y = on.empty((M, N), dtype)
+        else:
+            _operand(y, "y", _OUT, (M, N), codes)
+        workspace = _scratch(on, workspace, lib.q4_gemm_mx_workspace(M, N, K), codes, "q4_gemm_mx")
+        st = lib.q4_gemm_mx(codes.data_ptr(), scales.data_ptr(), x.data_ptr(), y.data_ptr(), _TYPE[y.dtype],
+                            M, N, K, workspace.data_ptr(), workspace.numel(), on.stream)
+    _check(st, "q4_gemm_mx")
+    return y
+
+
+def q4_gemm_experts(codes: torch.Tensor, scales: torch.Tensor, x: torch.Tensor, offsets: torch.Tensor,
+                    rows: torch.Tensor = None, y: torch.Tensor = None, N: int = None,
+                    dtype: torch.dtype = torch.float32, workspace: torch.Tensor = None,
+                    stream=None) -> torch.Tensor:
+    """y [T, N]: row p is x[rows[p]] @ W[e]^T for offsets[e] <= p <
+    offsets[e + 1], with W [E] a stack of microscaled matrices, offsets
+    [E + 1] and rows [T] int32 as q4_sort_experts makes them; zero for p >=
+    offsets[E].  Without rows, x [T, K] is taken in order.  Other arguments as
+    q4_gemm_mx."""
+    _dims(x, "x", (2,), "[rows of x, K]")
+    Mx, K = x.shape
+    E, N, K = _mx_sizes(codes, scales, N, K)
+    if E is None:
+        raise ValueError("codes is one matrix: use q4_gemm_mx, or codes[None] and scales[None]")
+    _operand(x, "x", _BF16, x.shape, codes)
+    _operand(offsets, "offsets", _I32, (E + 1,), codes)
+    T = Mx
+    if rows is not None:
+        _dims(rows, "rows", (1,), "[T]")
+        _operand(rows, "rows", _I32, rows.shape, codes)
+        T = rows.shape[0]
+    lib = load()
+    with _On(codes, stream) as on:
+        if y is None:
+            _type(dtype, _OUT, "dtype")
+            y = on.empty((T, N), dtype)
+        else:
+            _operand(y, "y", _OUT, (T, N), codes)
+        workspace = _scratch(on, workspace, lib.q4_gemm_experts_workspace(T, E, N, K), codes, "q4_gemm_experts")
+        st = lib.q4_gemm_experts(codes.data_ptr(), scales.data_ptr(), x.data_ptr(),
+                                 None if rows is None else rows.data_ptr(), offsets.data_ptr(),
+                                 y.data_ptr(), _TYPE[y.dtype], Mx, T, E, N, K, workspace.data_ptr(),
+                                 workspace.numel(), on.stream)
+    _check(st, "q4_gemm_experts")
+    return y
+
+
+def q4_sort_experts(ids: torch.Tensor, E: int, offsets: torch.Tensor = None, rows: torch.Tensor = None,
+                    places: torch.Tensor = None, stream=None):
+    """(offsets [E + 1], rows [T], places [M, top]), all int32: the stable order
+    by expert of the choices ids [M, top] (int32 or int64), T = M * top.  Ids
+    outside 0 .. E - 1 drop their choice: rows -1, places -1 - position."""
+    _dims(ids, "ids", (2,), "[M, top]")
+    M, top = ids.shape
+    E = int(E)
+    _operand(ids, "ids", _IDS, ids.shape, ids)
+    if E < 1 or top < 1:
+        raise ValueError(f"E = {E} and top = {top} must be at least 1")
+    with _On(ids, stream) as on:
+        if offsets is None:
+            offsets = on.empty(E + 1, torch.int32)
+        else:
+            _operand(offsets, "offsets", _I32, (E + 1,), ids)
+        if rows is None:
+            rows = on.empty(M * top, torch.int32)
+        else:
+            _operand(rows, "rows", _I32, (M * top,), ids)
+        if places is None:
+            places = on.empty((M, top), torch.int32)
+        else:
+            _operand(places, "places", _I32, (M, top), ids)
+        st = load().q4_sort_experts(ids.data_ptr(), int(ids.dtype == torch.int64), offsets.data_ptr(),
+                                    rows.data_ptr(), places.data_ptr(), M, top, E, on.stream)
+    _check(st, "q4_sort_experts")
+    return offsets, rows, places
+
+
+def _row_sizes(t, name, places, rows_of_tokens: bool):
+    """(M, top, K) of a row array and its places; the array has M rows, or M * top."""
+    _dims(places, "places", (2,), "[M, top]")
+    M, top = places.shape
+    _dims(t, name, (2,), "[M, K]" if rows_of_tokens else "[M * top, K]")
+    K = t.shape[1]
+    _operand(t, name, _FLOATS, (M if rows_of_tokens else M * top, K), t)
+    _operand(places, "places", _I32, places.shape, t)
+    return M, top, K
+
+
+def q4_dispatch(x: torch.Tensor, places: torch.Tensor, xs: torch.Tensor = None, stream=None) -> torch.Tensor:
+    """xs [M * top, K]: the rows of x [M, K] at their choices' places, zeros at
+    dropped ones.  The gradient is q4_combine(dxs, places)."""
+    M, top, K = _row_sizes(x, "x", places, True)
+    with _On(x, stream) as on:
+        if xs is None:
+            xs = on.empty((M * top, K), x.dtype)
+        else:
+            _operand(xs, "xs", (x.dtype,), (M * top, K), x)
+        st = load().q4_dispatch(x.data_ptr(), places.data_ptr(), xs.data_ptr(), _TYPE[x.dtype], M, top, K,
+                                on.stream)
+    _check(st, "q4_dispatch")
+    return xs
+
+
+def q4_combine(ys: torch.Tensor, places: torch.Tensor, weights: torch.Tensor = None,
+               out: torch.Tensor = None, stream=None) -> torch.Tensor:
+    """out [M, K] = sum over a token's kept choices of weights[m, j] (float32;
+    1 if None) * ys[places[m, j]], summed in float32.  The gradient is
+    q4_combine_grad, without weights q4_dispatch(dout, places)."""
+    M, top, K = _row_sizes(ys, "ys", places, False)
+    if weights is not None:
+        _operand(weights, "weights", _F32, (M, top), ys)
+    with _On(ys, stream) as on:
+        if out is None:
+            out = on.empty((M, K), ys.dtype)
+        else:
+            _operand(out, "out", (ys.dtype,), (M, K), ys)
+        st = load().q4_combine(ys.data_ptr(), places.data_ptr(), None if weights is None else weights.data_ptr(),
+                               out.data_ptr(), _TYPE[ys.dtype], M, top, K, on.stream)
+    _check(st, "q4_combine")
+    return out
+
+
+def q4_combine_grad(dout: torch.Tensor, ys: torch.Tensor, places: torch.Tensor, weights: torch.Tensor,
+                    dys: torch.Tensor = None, dweights: torch.Tensor = None, stream=None):
+    """(dys [M * top, K], dweights [M, top] float32): the gradients of
+    q4_combine(ys, places, weights) for dout [M, K]; zeros for dropped choices."""
+    M, top, K = _row_sizes(ys, "ys", places, False)
+    _operand(dout, "dout", (ys.dtype,), (M, K), ys)
+    _operand(weights, "weights", _F32, (M, top), ys)
+    with _On(ys, stream) as on:
+        if dys is None:
+            dys = on.empty((M * top, K), ys.dtype)
+        else:
+            _operand(dys, "dys", (ys.dtype,), (M * top, K), ys)
+        if dweights is None:
+            dweights = on.empty((M, top), torch.float32)
+        else:
+            _operand(dweights, "dweights", _F32, (M, top), ys)
+        st = load().q4_combine_grad(dout.data_ptr(), ys.data_ptr(), places.data_ptr(), weights.data_ptr(),
+                                    dys.data_ptr(), dweights.data_ptr(), _TYPE[ys.dtype], M, top, K, on.stream)
+    _check(st, "q4_combine_grad")
+    return dys, dweights
 
 
 def ring_slot_bytes(N: int, K: int) -> int:

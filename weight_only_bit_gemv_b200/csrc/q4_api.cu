@@ -4,12 +4,13 @@
 #include <mutex>
 
 #include "q4_internal.cuh"
+#include "q4_mx.cuh"
 
 namespace q4 {
 namespace {
 
 constexpr int kMaxDevices = 64;
-constexpr int kMaxSlots = 96;
+constexpr int kMaxSlots = 112;
 
 struct Cache {
     std::mutex mu;
@@ -421,10 +422,10 @@ q4_status q4_bounds_flags(uint32_t* flags) {
     if (!flags) return Q4_ERR_NULL;
     *flags = 0;
     cudaError_t e = cudaDeviceSynchronize();
-    cudaError_t (*const take[6])(unsigned int*) = {take_bounds_gemv_m1, take_bounds_gemm_small,
-                                                   take_bounds_gemm_tc, take_bounds_gemv,
-                                                   take_bounds_pack, take_bounds_gemv2};
-    for (int i = 0; i < 6 && e == cudaSuccess; ++i) {
+    cudaError_t (*const take[9])(unsigned int*) = {
+        take_bounds_gemv_m1, take_bounds_gemm_small, take_bounds_gemm_tc, take_bounds_gemv, take_bounds_pack,
+        take_bounds_gemv2,   take_bounds_mx_pack,    take_bounds_mx_gemm, take_bounds_experts};
+    for (int i = 0; i < 9 && e == cudaSuccess; ++i) {
         unsigned int v = 0;
         e = take[i](&v);
         if (v) *flags |= 1u << i;
@@ -449,7 +450,7 @@ const char* q4_status_string(q4_status status) {
         case Q4_ERR_ARCH: return "Q4_ERR_ARCH: the current device is not sm_100";
         case Q4_ERR_CUDA: return "Q4_ERR_CUDA: a CUDA call or kernel launch failed";
         case Q4_ERR_TOO_LARGE:
-            return "Q4_ERR_TOO_LARGE: 2 * M * K bytes exceed Q4_NOALLOC_SCRATCH_BYTES (q4_gemm_noalloc)";
+            return "Q4_ERR_TOO_LARGE: the work does not fit its scratch, slot or workspace";
     }
     return "unknown q4_status";
 }
@@ -505,14 +506,164 @@ q4_status q4_gemv2(const uint8_t* codes, const uint16_t* scales, const uint16_t*
 q4_status q4_timeout_flags(uint32_t* flags) {
     if (!flags) return Q4_ERR_NULL;
     *flags = 0;
-    unsigned int a = 0, b = 0, c = 0, d = 0;
+    unsigned int a = 0, b = 0, c = 0, d = 0, m = 0;
     cudaError_t e = take_gemv_m1_error(&a);
     if (e == cudaSuccess) e = take_gemm_tc_error(&b);
     if (e == cudaSuccess) e = take_gemm_small_error(&c);
     if (e == cudaSuccess) e = take_gemv2_error(&d);
+    if (e == cudaSuccess) e = take_gemm_mx_error(&m);
     if (e != cudaSuccess) return cuda_fail(e);
-    *flags = (a & 0x0FF0u) | (d & 0x000Eu) | ((c & 0x0F00u) << 4) | ((b & 0xFFFFu) << 16);
+    *flags = (a & 0x0FF0u) | (d & 0x000Eu) | ((c & 0x0F00u) << 4) | ((b & 0xFFFFu) << 16) | (m ? 1u : 0u);
     return Q4_OK;
+}
+
+// ---- microscaled 4-bit matrices ---------------------------------------------
+
+static bool known_type(int t) { return t == Q4_F32 || t == Q4_BF16 || t == Q4_F16; }
+
+// Sizes of a stack of microscaled matrices.
+static q4_status check_mx(int64_t E, int64_t N, int64_t K) {
+    if (E < 0 || N < 0 || E > Q4_MAX_MN || N > Q4_MAX_MN || K < 1 || K > Q4_MAX_K) return Q4_ERR_SHAPE;
+    // E and blocks of one matrix are each below 2^38: the product is checked by division
+    const int64_t one = mx_blocks(N) * mx_blocks(K);
+    if (one > 0 && E > Q4_MX_MAX_BLOCKS / one) return Q4_ERR_SHAPE;
+    return Q4_OK;
+}
+
+q4_status q4_pack_mx(const void* w, q4_type w_type, uint8_t* codes, uint8_t* scales, int64_t E, int64_t N,
+                     int64_t K, q4_stream_t stream) {
+    q4_status st = check_mx(E, N, K);
+    if (st != Q4_OK) return st;
+    if (!known_type(w_type)) return Q4_ERR_SHAPE;
+    if (E == 0 || N == 0) return Q4_OK;
+    if (!w || !codes || !scales) return Q4_ERR_NULL;
+    if (!aligned16(w) || !aligned16(codes) || !aligned16(scales)) return Q4_ERR_ALIGN;
+    DeviceInfo dev;
+    if ((st = gate(&dev)) != Q4_OK) return st;
+    return after_launch(launch_pack_mx(w, w_type, codes, scales, E, N, K, stream));
+}
+
+q4_status q4_dequant_mx(const uint8_t* codes, const uint8_t* scales, void* w_out, q4_type w_type, int64_t E,
+                        int64_t N, int64_t K, q4_stream_t stream) {
+    q4_status st = check_mx(E, N, K);
+    if (st != Q4_OK) return st;
+    if (!known_type(w_type)) return Q4_ERR_SHAPE;
+    if (E == 0 || N == 0) return Q4_OK;
+    if (!codes || !scales || !w_out) return Q4_ERR_NULL;
+    if (!aligned16(codes) || !aligned16(scales) || !aligned16(w_out)) return Q4_ERR_ALIGN;
+    DeviceInfo dev;
+    if ((st = gate(&dev)) != Q4_OK) return st;
+    return after_launch(launch_dequant_mx(codes, scales, w_out, w_type, E, N, K, stream));
+}
+
+static q4_status check_rows(int64_t Mx, int64_t T, int64_t E, int64_t N, int64_t K) {
+    const q4_status st = check_mx(E, N, K);
+    if (st != Q4_OK) return st;
+    if (E < 1 || E > Q4_MAX_EXPERTS || Mx < 0 || T < 0 || Mx > (1 << 30) || T > (1 << 30)) return Q4_ERR_SHAPE;
+    return Q4_OK;
+}
+
+int64_t q4_gemm_experts_workspace(int64_t T, int64_t E, int64_t N, int64_t K) {
+    if (check_rows(0, T, E, N, K) != Q4_OK) return -1;
+    return T == 0 || N == 0 ? 0 : static_cast<int64_t>(gemm_mx_workspace(T, E, N, K));
+}
+
+int64_t q4_gemm_mx_workspace(int64_t M, int64_t N, int64_t K) { return q4_gemm_experts_workspace(M, 1, N, K); }
+
+static q4_status run_gemm_mx(const uint8_t* codes, const uint8_t* scales, const uint16_t* x, const int32_t* rows,
+                             const int32_t* offsets, bool grouped, void* y, q4_type y_type, int64_t Mx, int64_t T,
+                             int64_t E, int64_t N, int64_t K, void* workspace, int64_t workspace_bytes,
+                             q4_stream_t stream) {
+    q4_status st = check_rows(Mx, T, E, N, K);
+    if (st != Q4_OK) return st;
+    if (y_type != Q4_F32 && y_type != Q4_BF16) return Q4_ERR_SHAPE;
+    if (T == 0 || N == 0) return Q4_OK;
+    if (grouped && !rows && Mx != T) return Q4_ERR_SHAPE;
+    if (!codes || !scales || !x || !y || !workspace || (grouped && !offsets)) return Q4_ERR_NULL;
+    if ((reinterpret_cast<uintptr_t>(codes) & 31u) || !aligned16(scales) || !aligned16(x) || !aligned16(rows) ||
+        !aligned16(offsets) || !aligned16(y) || !aligned16(workspace))
+        return Q4_ERR_ALIGN;
+    if (workspace_bytes < static_cast<int64_t>(gemm_mx_workspace(T, E, N, K))) return Q4_ERR_TOO_LARGE;
+    DeviceInfo dev;
+    if ((st = gate(&dev)) != Q4_OK) return st;
+    return after_launch(
+        launch_gemm_mx(codes, scales, x, rows, offsets, y, y_type, Mx, T, E, N, K, workspace, stream, dev));
+}
+
+q4_status q4_gemm_mx(const uint8_t* codes, const uint8_t* scales, const uint16_t* x, void* y, q4_type y_type,
+                     int64_t M, int64_t N, int64_t K, void* workspace, int64_t workspace_bytes,
+                     q4_stream_t stream) {
+    return run_gemm_mx(codes, scales, x, nullptr, nullptr, false, y, y_type, M, M, 1, N, K, workspace,
+                       workspace_bytes, stream);
+}
+
+q4_status q4_gemm_experts(const uint8_t* codes, const uint8_t* scales, const uint16_t* x, const int32_t* rows,
+                          const int32_t* offsets, void* y, q4_type y_type, int64_t Mx, int64_t T, int64_t E,
+                          int64_t N, int64_t K, void* workspace, int64_t workspace_bytes, q4_stream_t stream) {
+    return run_gemm_mx(codes, scales, x, rows, offsets, true, y, y_type, Mx, T, E, N, K, workspace,
+                       workspace_bytes, stream);
+}
+
+// ---- tokens sorted by expert and back ----------------------------------------
+
+static q4_status check_choices(int64_t M, int64_t top) {
+    if (M < 0 || top < 1 || M > Q4_MAX_MN || top > Q4_MAX_MN || M > Q4_MAX_MN / top) return Q4_ERR_SHAPE;
+    return Q4_OK;
+}
+
+static q4_status check_row_call(int type, int64_t M, int64_t top, int64_t K) {
+    const q4_status st = check_choices(M, top);
+    if (st != Q4_OK) return st;
+    return known_type(type) && K >= 1 && K <= Q4_MAX_K ? Q4_OK : Q4_ERR_SHAPE;
+}
+
+q4_status q4_sort_experts(const void* ids, int wide, int32_t* offsets, int32_t* rows, int32_t* places, int64_t M,
+                          int64_t top, int64_t E, q4_stream_t stream) {
+    q4_status st = check_choices(M, top);
+    if (st != Q4_OK) return st;
+    if (E < 1 || E > Q4_MAX_EXPERTS) return Q4_ERR_SHAPE;
+    if (!offsets || (M > 0 && (!ids || !rows || !places))) return Q4_ERR_NULL;
+    if (!aligned16(ids) || !aligned16(offsets) || !aligned16(rows) || !aligned16(places)) return Q4_ERR_ALIGN;
+    DeviceInfo dev;
+    if ((st = gate(&dev)) != Q4_OK) return st;
+    if (M == 0)
+        return after_launch(cudaMemsetAsync(offsets, 0, static_cast<size_t>(E + 1) * sizeof(int32_t), stream));
+    return after_launch(launch_sort_experts(ids, wide, offsets, rows, places, M, top, E, stream, dev));
+}
+
+q4_status q4_dispatch(const void* x, const int32_t* places, void* xs, q4_type type, int64_t M, int64_t top,
+                      int64_t K, q4_stream_t stream) {
+    q4_status st = check_row_call(type, M, top, K);
+    if (st != Q4_OK || M == 0) return st;
+    if (!x || !places || !xs) return Q4_ERR_NULL;
+    if (!aligned16(x) || !aligned16(places) || !aligned16(xs)) return Q4_ERR_ALIGN;
+    DeviceInfo dev;
+    if ((st = gate(&dev)) != Q4_OK) return st;
+    return after_launch(launch_dispatch(x, places, xs, type, M, top, K, stream));
+}
+
+q4_status q4_combine(const void* ys, const int32_t* places, const float* weights, void* out, q4_type type,
+                     int64_t M, int64_t top, int64_t K, q4_stream_t stream) {
+    q4_status st = check_row_call(type, M, top, K);
+    if (st != Q4_OK || M == 0) return st;
+    if (!ys || !places || !out) return Q4_ERR_NULL;
+    if (!aligned16(ys) || !aligned16(places) || !aligned16(weights) || !aligned16(out)) return Q4_ERR_ALIGN;
+    DeviceInfo dev;
+    if ((st = gate(&dev)) != Q4_OK) return st;
+    return after_launch(launch_combine(ys, places, weights, out, type, M, top, K, stream));
+}
+
+q4_status q4_combine_grad(const void* dout, const void* ys, const int32_t* places, const float* weights, void* dys,
+                          float* dweights, q4_type type, int64_t M, int64_t top, int64_t K, q4_stream_t stream) {
+    q4_status st = check_row_call(type, M, top, K);
+    if (st != Q4_OK || M == 0) return st;
+    if (!dout || !ys || !places || !weights || !dys || !dweights) return Q4_ERR_NULL;
+    if (!aligned16(dout) || !aligned16(ys) || !aligned16(places) || !aligned16(weights) || !aligned16(dys) ||
+        !aligned16(dweights))
+        return Q4_ERR_ALIGN;
+    DeviceInfo dev;
+    if ((st = gate(&dev)) != Q4_OK) return st;
+    return after_launch(launch_combine_grad(dout, ys, places, weights, dys, dweights, type, M, top, K, stream));
 }
 
 }  // extern "C"

@@ -1,0 +1,776 @@
+// q4_mx_gemm.cu -- products with microscaled 4-bit matrices: q4_gemm_mx (one
+// matrix) and q4_gemm_experts (rows grouped by expert, one matrix per group).
+//
+// Mathematics.  y[m][n] = sum_k W[n][k] x[m][k], W = e2m1 * 2^e with one e for
+// 32 k, x bfloat16.  The tensor cores multiply such blocks natively
+// (tcgen05.mma kind::mxf8f6f4, a scale factor per row and 32 k on either
+// side), so W's codes and exponents go from memory to the tensor core as
+// they are stored; nothing is decoded.  x, with 8 significant bits, is split
+// into two e4m3 parts with exponents per 32 k of their own:
+//     s = 2^(floor(log2 max|x|) - 7),  hi = e4m3(x / s),
+//     lo = e4m3((x / s - hi) * 32),    x = s * hi + (s / 32) * lo.
+// hi takes the leading 4 significant bits, and the remainder's bits fit lo
+// exactly wherever |x| >= 2^-14 of the group's largest; a smaller x is off by
+// at most half of lo's smallest step, 2^-15 s or 2^-22 of that largest.  Products are exact.  The tensor core
+// adds them to its binary32 accumulator by truncation: measured, the relative
+// error grows by 7e-8 for each 128 k.  For a binary32 y the accumulator is
+// therefore read out every kFlush32 blocks of k and added up in registers,
+// rounded to nearest (5e-7 measured at K = 1024); a bfloat16 y, whose own
+// rounding is 2^-9, takes kFlush16 blocks at a time.
+//
+// Work.  The hi rows and lo rows of kTokens tokens are the N = 2 kTokens
+// columns of one MMA, 128 rows of W its M; the epilogue adds the two halves.
+// An output tile is (expert, 128 rows of W, kTokens tokens) and its K is Kb
+// blocks; all tiles' blocks form one list of units, cut into equal runs, one
+// per persistent CTA, so few tiles still use every SM and there is no tail.
+// Where a tile is cut, each CTA stores its part to the workspace and counts
+// itself in; the last to come adds all parts in CTA order, so results do not
+// depend on timing and no CTA waits for another.
+//
+// Roles in a CTA: warp 0 streams stages of one k block (codes by a TMA load
+// that spreads 16 nibbles over 16 bytes, exponents by bulk copies, x parts by
+// TMA); warp 1 copies the exponents to tensor memory and issues four MMAs per
+// block; warps 2-5 read the accumulator and write y.  For few tokens the
+// stream of codes bounds it: one block costs 8.7 KB of HBM and about 200
+// cycles of MMA.  The weights' first stages are requested before the x
+// conversion that precedes on the stream has finished (programmatic
+// dependent launch).
+// Every wait is bounded; one that runs out sets an error bit and the CTA
+// drains its copies, frees its tensor memory and exits.
+#include <algorithm>
+
+#include "q4_mx.cuh"
+#include "q4_sm100.cuh"
+
+namespace q4 {
+
+__device__ unsigned int g_gemm_mx_error;
+
+namespace {
+
+constexpr int kThreads = 192;     // producer, MMA, four epilogue warps
+constexpr int kFlush32 = 8;       // k blocks per accumulation in tensor memory, binary32 y
+constexpr int kFlush16 = 64;      // ... bfloat16 y
+constexpr int kMinUnits = 4;      // least k blocks a CTA is started for
+constexpr uint32_t kTmemCols = 512;
+constexpr int kMaxExperts = Q4_MAX_EXPERTS;
+
+struct MxGemm {
+    const uint8_t* codes_scales;  // exponent bytes of W
+    const uint8_t* xsf;           // exponent bytes of x's parts, [tile][kXBlocks][Kb][512]
+    const int32_t* offsets;       // first row of each expert; nullptr: one matrix
+    float* partial;               // [2 * CTAs][kTokens][128]
+    uint32_t* counters;           // [tiles]
+    void* y;
+    int64_t N;
+    int64_t tile_limit;           // token tiles that the workspace holds
+    int T, E, Nb, Kb, y_bf16, flush;
+};
+
+// Layout of the workspace, all parts multiples of 1024 bytes.
+struct Workspace {
+    int64_t tiles;  // bound on the number of token tiles
+    size_t counters, xq, xsf, partial, bytes;
+};
+
+int x_blocks(int tokens) { return (2 * tokens + kMxBlock - 1) / kMxBlock; }
+
+// Tokens per tile: the smallest tile that holds an expert's average share.
+// (Measured rule; see the table of tile sizes beside the launcher.)
+int tokens_per_tile(int64_t T, int64_t E) {
+    const int64_t share = (T + E - 1) / E;
+    for (int t = 8; t < 128; t *= 2)
+        if (share <= t) return t;
+    return 128;
+}
+
+Workspace workspace_layout(int64_t T, int64_t E, int64_t N, int64_t K, int tokens) {
+    auto up = [](size_t n) { return (n + 1023) / 1024 * 1024; };
+    const int64_t Nb = mx_blocks(N), Kb = mx_blocks(K);
+    Workspace w{};
+    // an expert with c > 0 rows has at most c / tokens + 1 tiles
+    w.tiles = E == 1 ? (T + tokens - 1) / tokens : std::min(T, T / tokens + E);
+    w.counters = 0;
+    w.xq = up(static_cast<size_t>(w.tiles) * Nb * sizeof(uint32_t));
+    w.xsf = w.xq + up(static_cast<size_t>(w.tiles) * 2 * tokens * Kb * kMxBlock);
+    w.partial = w.xsf + up(static_cast<size_t>(w.tiles) * x_blocks(tokens) * Kb * kMxScaleBytes);
+    w.bytes = w.partial + up(static_cast<size_t>(2) * kMxMaxSms * tokens * kMxBlock * sizeof(float));
+    return w;
+}
+
+// ---------------------------------------------------------------------------
+// device helpers
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// 512 exponent bytes from shared memory to four columns of tensor memory,
+// repeated in the four lane quarters.
+__device__ __forceinline__ void tc_copy_scales(uint32_t taddr, uint64_t desc) {
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+
+// D[tmem] (+)= (A * sfa) x (B * sfb)^T, both operands in shared memory.
+__device__ __forceinline__ void tc_mma_mx(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
+                                          uint32_t sfb, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+}
+
+// Descriptor of 32 rows of 16 bytes in a row (no swizzle), for tc_copy_scales.
+__device__ __forceinline__ uint64_t scale_desc(uint32_t saddr) {
+    return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (1ull << 16) | (static_cast<uint64_t>(128 >> 4) << 32) |
+           (1ull << 46);
+}
+
+// Instruction descriptor: A e2m1, B e4m3, power-of-two scales, M = 128; the
+// scale byte q of each 32-bit column is taken on both sides.
+constexpr uint32_t mx_idesc(int N, int q) {
+    return (static_cast<uint32_t>(q) << 4) | (5u << 7) | (0u << 10) | (static_cast<uint32_t>(N >> 3) << 17) |
+           (1u << 23) | ((128u >> 4) << 24) | (static_cast<uint32_t>(q) << 29);
+}
+
+// Barrier of the four epilogue warps; true if `ok` was true in all of them.
+// They leave their loop only on its result, so none waits for one that left.
+__device__ __forceinline__ bool epilogue_sync(bool ok) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.and.pred q, 1, 128, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(ok ? 1u : 0u)
+        : "memory");
+    return r != 0u;
+}
+
+// Row ranges of the experts and the token tiles before each, in shared
+// memory: offset[e], tile[e] for e in [0, E].  Offsets are taken as
+// non-decreasing values in [0, T]; anything else is clamped to that.
+struct Table {
+    int offset[kMaxExperts + 1];
+    int tile[kMaxExperts + 1];
+};
+
+template <int kTokens>
+__device__ void fill_table(Table& t, const int32_t* __restrict__ offsets, int E, int T) {
+    if (!offsets) {
+        if (threadIdx.x == 0) {
+            t.offset[0] = 0;
+            t.offset[1] = T;
+            t.tile[0] = 0;
+            t.tile[1] = (T + kTokens - 1) / kTokens;
+        }
+    } else if (threadIdx.x < 32) {
+        const int lane = threadIdx.x;
+        int high = 0, tiles = 0;  // over the experts before this round
+        for (int e0 = 0; e0 < E; e0 += 32) {
+            const int e = e0 + lane;
+            int first = e < E && Q4_IN_BOUNDS(e, 2, E + 1) ? min(max(__ldg(offsets + e), 0), T) : 0;
+            int last = e < E ? min(max(__ldg(offsets + e + 1), 0), T) : 0;
+            // running maxima: first is at least every earlier end
+            int top = max(first, last);
+#pragma unroll
+            for (int d = 1; d < 32; d *= 2) {
+                const int o = __shfl_up_sync(0xFFFFFFFFu, top, d);
+                if (lane >= d) top = max(top, o);
+            }
+            const int up = __shfl_up_sync(0xFFFFFFFFu, top, 1);
+            const int before = max(high, lane ? up : 0);
+            first = max(first, before);
+            last = max(last, first);
+            const int mine = e < E ? (last - first + kTokens - 1) / kTokens : 0;
+            int sum = mine;
+#pragma unroll
+            for (int d = 1; d < 32; d *= 2) {
+                const int o = __shfl_up_sync(0xFFFFFFFFu, sum, d);
+                if (lane >= d) sum += o;
+            }
+            if (e < E) {
+                t.offset[e] = first;
+                t.tile[e] = tiles + sum - mine;
+                if (e == E - 1) {
+                    t.offset[E] = last;
+                    t.tile[E] = tiles + sum;
+                }
+            }
+            high = max(high, __shfl_sync(0xFFFFFFFFu, top, 31));
+            tiles += __shfl_sync(0xFFFFFFFFu, sum, 31);
+        }
+    }
+    __syncthreads();
+}
+
+// The last e with first[e] <= v (first[0] <= v < first[E]).
+__device__ __forceinline__ int find_expert(const int* first, int E, int v) {
+    int lo = 0, hi = E;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (first[mid] <= v)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    return lo;
+}
+
+// ---------------------------------------------------------------------------
+// x to its two e4m3 parts, in the order of the token tiles
+// ---------------------------------------------------------------------------
+// Eight binary32 values to e4m3 and back.
+__device__ __forceinline__ uint32_t to_e4m3x2(float a, float b) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %2, %1;" : "=h"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 from_e4m3x2(uint32_t v) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(v)));
+    return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+
+struct Convert {
+    const uint16_t* x;
+    const int32_t* rows;  // x row of each of the T rows; nullptr: the row itself
+    const int32_t* offsets;
+    uint8_t* xq;
+    uint8_t* xsf;
+    uint32_t* counters;
+    void* y;
+    int64_t Mx, K, N, counter_count, tile_limit;
+    int T, E, Kb, y_bf16;
+};
+
+// One warp converts 256 k of one row: 4 lanes a group of 32, 8 values a lane.
+template <int kTokens, bool kVector>
+__global__ void __launch_bounds__(256) convert_kernel(const Convert p) {
+    constexpr int kXBlocks = (2 * kTokens + kMxBlock - 1) / kMxBlock;
+    __shared__ Table table;
+    pdl_launch();
+    fill_table<kTokens>(table, p.offsets, p.E, p.T);
+    const int64_t thread = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x;
+    const int64_t threads = static_cast<int64_t>(gridDim.x) * blockDim.x;
+    for (int64_t i = thread; i < p.counter_count; i += threads) p.counters[i] = 0;
+    // rows of y behind the last expert's
+    const int64_t behind = table.offset[p.E] * p.N, all = static_cast<int64_t>(p.T) * p.N;
+    for (int64_t i = behind + thread; i < all; i += threads) {
+        if (!Q4_IN_BOUNDS(i, 1, all)) continue;
+        if (p.y_bf16)
+            static_cast<uint16_t*>(p.y)[i] = 0;
+        else
+            static_cast<float*>(p.y)[i] = 0.0f;
+    }
+    const int lane = threadIdx.x & 31;
+    const int pieces = (p.Kb + 1) / 2;  // runs of 256 k
+    const int64_t jobs = static_cast<int64_t>(table.offset[p.E]) * pieces;
+    for (int64_t job = thread / 32; job < jobs; job += threads / 32) {
+        const int row = static_cast<int>(job / pieces), piece = static_cast<int>(job % pieces);
+        const int e = find_expert(table.offset, p.E, row);
+        const int in = row - table.offset[e];
+        const int64_t tile = table.tile[e] + in / kTokens;
+        if (row < table.offset[0] || tile >= p.tile_limit) continue;  // offsets that do not start at 0
+        const int m = in % kTokens;
+        const int64_t src = p.rows ? static_cast<int64_t>(__ldg(p.rows + row)) : row;
+        const bool have = src >= 0 && src < p.Mx;
+        const int64_t k = piece * 256 + 8 * lane;
+        const int kb = 2 * piece + lane / 16;
+        float v[8];
+        if (kVector) {
+            uint4 q = make_uint4(0, 0, 0, 0);
+            if (have && k < p.K && Q4_IN_BOUNDS(src * p.K + k, 8, p.Mx * p.K))
+                q = __ldg(reinterpret_cast<const uint4*>(p.x + src * p.K + k));
+            const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                v[2 * j] = __uint_as_float(w[j] << 16);
+                v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                v[j] = have && k + j < p.K && Q4_IN_BOUNDS(src * p.K + k + j, 1, p.Mx * p.K)
+                           ? bf16_bits_to_float(p.x[src * p.K + k + j]) : 0.0f;
+        }
+        uint32_t top = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+        top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+        top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+        // hi's exponent byte: the largest value's field - 7, so that the
+        // largest x / s is in [128, 256); at least 5, which leaves lo's >= 0
+        const uint32_t field = top >> 23;
+        const uint32_t byte = field > 12u ? field - 7u : 5u;
+        const float inverse = __uint_as_float((254u - byte) << 23);
+        uint2 hi, lo;
+        uint32_t* hp = &hi.x;
+        uint32_t* lp = &lo.x;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            uint32_t h = 0, l = 0;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float a = v[4 * j + 2 * i] * inverse, b = v[4 * j + 2 * i + 1] * inverse;
+                const uint32_t c = to_e4m3x2(a, b);
+                const float2 back = from_e4m3x2(c);
+                h |= c << (16 * i);
+                l |= to_e4m3x2((a - back.x) * 32.0f, (b - back.y) * 32.0f) << (16 * i);
+            }
+            hp[j] = h;
+            lp[j] = l;
+        }
+        if (kb < p.Kb) {
+            const int64_t Kp = static_cast<int64_t>(p.Kb) * kMxBlock;
+            [[maybe_unused]] const int64_t extent = p.tile_limit * 2 * kTokens * Kp;
+            const int64_t at = (tile * 2 * kTokens + m) * Kp + k;
+            if (Q4_IN_BOUNDS(at, 8, extent) && Q4_IN_BOUNDS(at + kTokens * Kp, 8, extent)) {
+                *reinterpret_cast<uint2*>(p.xq + at) = hi;
+                *reinterpret_cast<uint2*>(p.xq + at + kTokens * Kp) = lo;
+            }
+        }
+        // the four groups of a k block: one 32-bit store per part.  A group
+        // with an infinity or NaN gets the exponent byte of NaN.
+        const uint32_t mine = field == 255u ? 255u : byte;
+        uint32_t four = 0, four_lo = 0;
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            const uint32_t b = __shfl_sync(0xFFFFFFFFu, mine, (lane & 16) + 4 * g);
+            four |= b << (8 * g);
+            four_lo |= (b == 255u ? 255u : b - 5u) << (8 * g);
+        }
+        if ((lane & 15) == 0 && kb < p.Kb) {
+            [[maybe_unused]] const int64_t extent = p.tile_limit * kXBlocks * p.Kb * kMxScaleBytes;
+            const int r = kTokens + m;
+            const int64_t at = ((tile * kXBlocks + m / kMxBlock) * p.Kb + kb) * kMxScaleBytes + mx_scale_at(m % kMxBlock, 0);
+            const int64_t at_lo =
+                ((tile * kXBlocks + r / kMxBlock) * p.Kb + kb) * kMxScaleBytes + mx_scale_at(r % kMxBlock, 0);
+            if (Q4_IN_BOUNDS(at, 4, extent) && Q4_IN_BOUNDS(at_lo, 4, extent)) {
+                *reinterpret_cast<uint32_t*>(p.xsf + at) = four;
+                *reinterpret_cast<uint32_t*>(p.xsf + at_lo) = four_lo;
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// the product
+// ---------------------------------------------------------------------------
+template <int kTokens>
+struct Shape {
+    static constexpr int kCols = 2 * kTokens;                    // MMA N
+    static constexpr int kXBlocks = (kCols + kMxBlock - 1) / kMxBlock;
+    static constexpr int kABytes = kMxBlock * 128;               // codes spread over bytes
+    static constexpr int kBBytes = kCols * 128;
+    static constexpr int kStage = kABytes + kBBytes + kMxScaleBytes * (1 + kXBlocks);
+    static constexpr int kStagePitch = (kStage + 1023) / 1024 * 1024;
+    // bytes that complete on a stage's barrier: the load that spreads the
+    // nibbles counts the bytes it reads
+    static constexpr int kTx = kMxCodeBytes + kBBytes + kMxScaleBytes * (1 + kXBlocks);
+    static constexpr int kStages = (222 * 1024 - static_cast<int>(sizeof(Table))) / kStagePitch < 12
+                                       ? (222 * 1024 - static_cast<int>(sizeof(Table))) / kStagePitch : 12;
+    static constexpr int kBuffers = 2 * kCols + 32 <= 512 ? 2 : 1;  // accumulators
+    static constexpr uint32_t kScaleCol = kBuffers * kCols;        // two sets of exponent columns
+    static constexpr uint32_t kScaleSet = 4 * (1 + kXBlocks);
+    static constexpr int kSmem = 1024 + kStages * kStagePitch + static_cast<int>(sizeof(Table)) + 512;
+    static_assert(kStages >= 3, "the ring needs stages");
+    static_assert(kScaleCol + 2 * kScaleSet <= kTmemCols, "tensor memory");
+};
+
+// A CTA's run of units, a unit being one k block of one output tile.
+// Tiles are numbered by expert, then row block of W, then token tile, so that
+// the token tiles of one row block follow each other and find its codes in L2.
+struct Segment {
+    int64_t out;            // output tile
+    int e, nb, tile, in;    // expert, row block, token tile, its number in the expert
+    int k0, k1;
+};
+struct Runs {
+    int64_t units, u, u1;
+    int64_t ctas;
+    __device__ Runs(const MxGemm& p, const Table& t) {
+        const int64_t tiles = min(static_cast<int64_t>(t.tile[p.E]), p.tile_limit);
+        units = tiles * p.Nb * p.Kb;
+        ctas = min(static_cast<int64_t>(gridDim.x), max(units / kMinUnits, static_cast<int64_t>(1)));
+        u = blockIdx.x < ctas ? start(blockIdx.x) : units;
+        u1 = blockIdx.x < ctas ? start(blockIdx.x + 1) : units;
+    }
+    __device__ int64_t start(int64_t c) const { return units * c / ctas; }
+    // the CTA whose run holds unit v
+    __device__ int64_t owner(int64_t v) const { return ((v + 1) * ctas - 1) / units; }
+    __device__ bool next(const MxGemm& p, const Table& t, Segment& s) {
+        if (u >= u1) return false;
+        s.out = u / p.Kb;
+        s.k0 = static_cast<int>(u - s.out * p.Kb);
+        s.k1 = static_cast<int>(min(static_cast<int64_t>(p.Kb), s.k0 + u1 - u));
+        u += s.k1 - s.k0;
+        s.e = find_expert(t.tile, p.E, static_cast<int>(s.out / p.Nb));
+        const int64_t local = s.out - static_cast<int64_t>(t.tile[s.e]) * p.Nb;
+        const int mine = t.tile[s.e + 1] - t.tile[s.e];
+        s.nb = static_cast<int>(local / mine);
+        s.in = static_cast<int>(local % mine);
+        s.tile = t.tile[s.e] + s.in;
+        return true;
+    }
+};
+
+template <int kTokens>
+__global__ void __launch_bounds__(kThreads, 1)
+    gemm_mx_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
+                   const MxGemm p) {
+    using S = Shape<kTokens>;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    uint8_t* smem = smem_raw + (base - smem_u32(smem_raw));
+    Table& table = *reinterpret_cast<Table*>(smem + S::kStages * S::kStagePitch);
+    uint8_t* tail = smem + S::kStages * S::kStagePitch + sizeof(Table);
+    const uint32_t bars = (smem_u32(tail) + 7u) & ~7u;
+    auto full = [&](int s) { return bars + 8u * s; };
+    auto empty = [&](int s) { return bars + 8u * (S::kStages + s); };
+    auto dfull = [&](int b) { return bars + 8u * (2 * S::kStages + b); };
+    auto dempty = [&](int b) { return bars + 8u * (2 * S::kStages + 2 + b); };
+    const uint32_t drain = bars + 8u * (2 * S::kStages + 4);
+    const uint32_t words = bars + 8u * (2 * S::kStages + 5);  // tensor-memory base, abort, last arrival
+    volatile uint32_t* word = reinterpret_cast<volatile uint32_t*>(smem + (words - base));
+    volatile uint32_t* abort_flag = word + 1;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+    if (tid == 0) {
+        for (int s = 0; s < S::kStages; ++s) {
+            mbar_init(full(s), 1);
+            mbar_init(empty(s), 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(dfull(b), 1);
+            mbar_init(dempty(b), 4);
+        }
+        mbar_init(drain, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+        prefetch_tensor_map(&wmap);
+        prefetch_tensor_map(&xmap);
+    }
+    if (warp == 1) {
+        tmem_alloc(words, kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    fill_table<kTokens>(table, p.offsets, p.E, p.T);  // ends in __syncthreads
+    tc_fence_after();
+    const uint32_t tmem = *word;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            // ---------------------------- producer ----------------------------
+            int it = 0;
+            bool ok = true;
+            auto load_w = [&](const Segment& s, int k, int slot) {
+                const uint32_t dst = base + slot * S::kStagePitch;
+                const int64_t block = (static_cast<int64_t>(s.e) * p.Nb + s.nb) * p.Kb + k;
+                mbar_arrive_expect_tx(full(slot), S::kTx);
+                tma_load_2d(dst, &wmap, 0, static_cast<int>(block * kMxBlock), full(slot));
+                if (Q4_IN_BOUNDS(block, 1, static_cast<int64_t>(p.E) * p.Nb * p.Kb))
+                    bulk_load(dst + S::kABytes + S::kBBytes, p.codes_scales + block * kMxScaleBytes, kMxScaleBytes,
+                              full(slot));
+            };
+            auto load_x = [&](const Segment& s, int k, int slot) {
+                const uint32_t dst = base + slot * S::kStagePitch;
+                tma_load_2d(dst + S::kABytes, &xmap, k * kMxBlock, s.tile * S::kCols, full(slot));
+#pragma unroll
+                for (int b = 0; b < S::kXBlocks; ++b) {
+                    const int64_t at = (static_cast<int64_t>(s.tile) * S::kXBlocks + b) * p.Kb + k;
+                    if (Q4_IN_BOUNDS(at, 1, p.tile_limit * S::kXBlocks * p.Kb))
+                        bulk_load(dst + S::kABytes + S::kBBytes + kMxScaleBytes * (1 + b), p.xsf + at * kMxScaleBytes,
+                                  kMxScaleBytes, full(slot));
+                }
+            };
+            // the ring's first filling: W before the x conversion is known to be done
+            Segment s;
+            {
+                Runs runs(p, table);
+                for (int n = 0; n < S::kStages && runs.next(p, table, s);)
+                    for (int k = s.k0; k < s.k1 && n < S::kStages; ++k, ++n) load_w(s, k, n);
+            }
+            pdl_wait();
+            asm volatile("fence.proxy.async;" ::: "memory");  // x's parts were written by plain stores
+            Runs runs(p, table);
+            while (ok && runs.next(p, table, s)) {
+                for (int k = s.k0; k < s.k1; ++k, ++it) {
+                    const int slot = it % S::kStages;
+                    if (it >= S::kStages) {
+                        if (!mbar_wait(empty(slot), static_cast<uint32_t>(it / S::kStages - 1) & 1u) || *abort_flag) {
+                            ok = false;
+                            break;
+                        }
+                        load_w(s, k, slot);
+                    }
+                    load_x(s, k, slot);
+                }
+            }
+            if (!ok) {
+                atomicOr(&g_gemm_mx_error, 1u);
+                *abort_flag = 1;
+            }
+            // leave only once every copy issued has landed (bounded)
+            for (int i = it > S::kStages ? it - S::kStages : 0; i < it; ++i)
+                if (!mbar_wait(full(i % S::kStages), static_cast<uint32_t>(i / S::kStages) & 1u)) break;
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (lane == 0) {
+            // ------------------------------- MMA -------------------------------
+            int it = 0, fl = 0;  // stages, accumulations
+            bool ok = true;
+            Runs runs(p, table);
+            Segment s;
+            while (ok && runs.next(p, table, s)) {
+                for (int k0 = s.k0; ok && k0 < s.k1; k0 += p.flush, ++fl) {
+                    const int buf = fl % S::kBuffers, k1 = min(s.k1, k0 + p.flush);
+                    if (fl >= S::kBuffers &&
+                        !mbar_wait(dempty(buf), static_cast<uint32_t>(fl / S::kBuffers - 1) & 1u)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t d = tmem + buf * S::kCols;
+                    for (int k = k0; k < k1; ++k, ++it) {
+                        const int slot = it % S::kStages;
+                        if (!mbar_wait(full(slot), static_cast<uint32_t>(it / S::kStages) & 1u) || *abort_flag) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint32_t a = base + slot * S::kStagePitch, b = a + S::kABytes, sf = b + S::kBBytes;
+                        const uint32_t sfa = tmem + S::kScaleCol + (it & 1) * S::kScaleSet, sfb = sfa + 4;
+                        tc_copy_scales(sfa, scale_desc(sf));
+#pragma unroll
+                        for (int j = 0; j < S::kXBlocks; ++j)
+                            tc_copy_scales(sfb + 4 * j, scale_desc(sf + kMxScaleBytes * (1 + j)));
+                        const uint64_t ad = smem_desc_sw128(a, 1024), bd = smem_desc_sw128(b, 1024);
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            tc_mma_mx(d, ad + 2 * q, bd + 2 * q, mx_idesc(S::kCols, q), sfa, sfb,
+                                      (k > k0 || q > 0) ? 1u : 0u);
+                        tc_commit(empty(slot));
+                    }
+                    if (ok) tc_commit(dfull(buf));
+                }
+            }
+            if (!ok) {
+                atomicOr(&g_gemm_mx_error, 2u);
+                *abort_flag = 1;
+            }
+            tc_commit(drain);
+            if (!mbar_wait(drain, 0u)) atomicOr(&g_gemm_mx_error, 4u);
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------ epilogue ------------------------------
+        const int quarter = warp & 3, row = 32 * quarter + lane;
+        const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * quarter) << 16);
+        constexpr int kLoad = kTokens < 32 ? 8 : 32;  // columns per tensor-memory load
+        int fl = 0;
+        bool ok = true;
+        Runs runs(p, table);
+        Segment s;
+        pdl_wait();  // the counters' zeros, and whoever read the workspace before
+        while (ok && runs.next(p, table, s)) {
+            float acc[kTokens];
+#pragma unroll
+            for (int i = 0; i < kTokens; ++i) acc[i] = 0.0f;
+            for (int k0 = s.k0; k0 < s.k1; k0 += p.flush, ++fl) {
+                const int buf = fl % S::kBuffers;
+                if (!mbar_wait(dfull(buf), static_cast<uint32_t>(fl / S::kBuffers) & 1u) || *abort_flag) ok = false;
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                if (!ok) break;
+                tc_fence_after();
+#pragma unroll
+                for (int c = 0; c < kTokens; c += kLoad) {
+                    uint32_t hi[kLoad], lo[kLoad];
+                    if (kLoad == 8) {
+                        tc_ld_x8(lanes + buf * S::kCols + c, hi);
+                        tc_ld_x8(lanes + buf * S::kCols + kTokens + c, lo);
+                    } else {
+                        tc_ld_x32(lanes + buf * S::kCols + c, hi);
+                        tc_ld_x32(lanes + buf * S::kCols + kTokens + c, lo);
+                    }
+                    tc_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < kLoad; ++i) acc[c + i] += __uint_as_float(hi[i]) + __uint_as_float(lo[i]);
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(dempty(buf));
+            }
+            ok = epilogue_sync(ok);
+            if (!ok) break;
+            const int first = table.offset[s.e] + s.in * kTokens;
+            const int count = min(kTokens, table.offset[s.e + 1] - first);
+            const int64_t n = static_cast<int64_t>(s.nb) * kMxBlock + row;
+            [[maybe_unused]] const int64_t yextent = static_cast<int64_t>(p.T) * p.N;
+            auto store = [&](int m, float v) {
+                const int64_t at = static_cast<int64_t>(first + m) * p.N + n;
+                if (n >= p.N || !Q4_IN_BOUNDS(at, 1, yextent)) return;
+                if (p.y_bf16)
+                    static_cast<__nv_bfloat16*>(p.y)[at] = __float2bfloat16_rn(v);
+                else
+                    static_cast<float*>(p.y)[at] = v;
+            };
+            if (s.k0 == 0 && s.k1 == p.Kb) {
+#pragma unroll
+                for (int m = 0; m < kTokens; ++m)
+                    if (m < count) store(m, acc[m]);
+                continue;
+            }
+            // A part of a tile.  A run that begins inside the tile owns slot
+            // 2 c, one that begins with it (or before) slot 2 c + 1.
+            auto slot_of = [&](int64_t c, bool inside) { return p.partial + ((2 * c + (inside ? 0 : 1)) * kTokens) * kMxBlock + row; };
+            float* mine = slot_of(blockIdx.x, s.k0 > 0);
+#pragma unroll
+            for (int m = 0; m < kTokens; ++m)
+                if (m < count) __stcg(mine + m * kMxBlock, acc[m]);
+            __threadfence();
+            epilogue_sync(true);
+            const int64_t u0 = s.out * p.Kb;
+            const int64_t c0 = runs.owner(u0), c1 = runs.owner(u0 + p.Kb - 1);
+            if (tid == 64) word[2] = atomicAdd(p.counters + s.out, 1u) == static_cast<uint32_t>(c1 - c0) ? 1u : 0u;
+            epilogue_sync(true);
+            const bool last = word[2] != 0u;
+            if (!last) continue;
+            __threadfence();
+#pragma unroll
+            for (int i = 0; i < kTokens; ++i) acc[i] = 0.0f;
+            for (int64_t c = c0; c <= c1; ++c) {
+                const float* part = slot_of(c, runs.start(c) > u0);
+#pragma unroll
+                for (int m = 0; m < kTokens; ++m)
+                    if (m < count) acc[m] += __ldcg(part + m * kMxBlock);
+            }
+#pragma unroll
+            for (int m = 0; m < kTokens; ++m)
+                if (m < count) store(m, acc[m]);
+        }
+        if (!ok && lane == 0) {
+            atomicOr(&g_gemm_mx_error, 8u);
+            *abort_flag = 1;
+        }
+    }
+
+    // -------------------------------- teardown --------------------------------
+    pdl_wait();  // no CTA ends before the conversion has: it writes y's last rows
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+template <int kTokens>
+cudaError_t launch_as(const uint8_t* codes, const uint8_t* scales, const uint16_t* x, const int32_t* rows,
+                      const int32_t* offsets, void* y, int y_type, int64_t Mx, int64_t T, int64_t E, int64_t N,
+                      int64_t K, uint8_t* ws, cudaStream_t s, const DeviceInfo& dev) {
+    using S = Shape<kTokens>;
+    const Workspace l = workspace_layout(T, E, N, K, kTokens);
+    const int64_t Nb = mx_blocks(N), Kb = mx_blocks(K);
+    Convert c{};
+    c.x = x;
+    c.rows = rows;
+    c.offsets = offsets;
+    c.xq = ws + l.xq;
+    c.xsf = ws + l.xsf;
+    c.counters = reinterpret_cast<uint32_t*>(ws + l.counters);
+    c.y = y;
+    c.Mx = Mx;
+    c.K = K;
+    c.N = N;
+    c.counter_count = l.tiles * Nb;
+    c.tile_limit = l.tiles;
+    c.T = static_cast<int>(T);
+    c.E = static_cast<int>(E);
+    c.Kb = static_cast<int>(Kb);
+    c.y_bf16 = y_type == Q4_BF16;
+    const int64_t warps = std::max(T * ((Kb + 1) / 2), (c.counter_count + 255) / 256);
+    const int grid = static_cast<int>(std::min<int64_t>((warps + 7) / 8, dev.sm_count * 8));
+    if (K % 8 == 0)
+        convert_kernel<kTokens, true><<<grid, 256, 0, s>>>(c);
+    else
+        convert_kernel<kTokens, false><<<grid, 256, 0, s>>>(c);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+
+    CUtensorMap wmap, xmap;
+    e = encode_tensor_map_2d(&wmap, codes, CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, 0,
+                             static_cast<uint64_t>(E * Nb * Kb * kMxBlock), kMxBlock, 64, kMxBlock, kMxBlock,
+                             CU_TENSOR_MAP_SWIZZLE_128B);
+    if (e != cudaSuccess) return e;
+    e = encode_tensor_map_2d(&xmap, c.xq, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1,
+                             static_cast<uint64_t>(l.tiles * S::kCols), static_cast<uint64_t>(Kb * kMxBlock),
+                             static_cast<uint64_t>(Kb * kMxBlock), S::kCols, 128, CU_TENSOR_MAP_SWIZZLE_128B);
+    if (e != cudaSuccess) return e;
+    MxGemm p{};
+    p.codes_scales = scales;
+    p.xsf = c.xsf;
+    p.offsets = offsets;
+    p.partial = reinterpret_cast<float*>(ws + l.partial);
+    p.counters = c.counters;
+    p.y = y;
+    p.N = N;
+    p.tile_limit = l.tiles;
+    p.T = c.T;
+    p.E = c.E;
+    p.Nb = static_cast<int>(Nb);
+    p.Kb = c.Kb;
+    p.y_bf16 = c.y_bf16;
+    p.flush = c.y_bf16 ? kFlush16 : kFlush32;
+    const void* fn = reinterpret_cast<const void*>(gemm_mx_kernel<kTokens>);
+    constexpr int kSlot = kTokens == 8 ? 100 : kTokens == 16 ? 101 : kTokens == 32 ? 102 : kTokens == 64 ? 103 : 104;
+    if (S::kSmem > dev.smem_optin) return cudaErrorNotSupported;
+    e = ensure_smem_attr(fn, S::kSmem, kSlot, dev.device);
+    if (e != cudaSuccess) return e;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(
+        std::min(dev.sm_count, kMxMaxSms), std::max<int64_t>(1, l.tiles * Nb * Kb / kMinUnits))));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = S::kSmem;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, gemm_mx_kernel<kTokens>, wmap, xmap, p);
+}
+
+}  // namespace
+
+size_t gemm_mx_workspace(int64_t T, int64_t E, int64_t N, int64_t K) {
+    return workspace_layout(T, E, N, K, tokens_per_tile(T, E)).bytes;
+}
+
+cudaError_t launch_gemm_mx(const uint8_t* codes, const uint8_t* scales, const uint16_t* x, const int32_t* rows,
+                           const int32_t* offsets, void* y, int y_type, int64_t Mx, int64_t T, int64_t E, int64_t N,
+                           int64_t K, void* workspace, cudaStream_t s, const DeviceInfo& dev) {
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    switch (tokens_per_tile(T, E)) {
+        case 8: return launch_as<8>(codes, scales, x, rows, offsets, y, y_type, Mx, T, E, N, K, ws, s, dev);
+        case 16: return launch_as<16>(codes, scales, x, rows, offsets, y, y_type, Mx, T, E, N, K, ws, s, dev);
+        case 32: return launch_as<32>(codes, scales, x, rows, offsets, y, y_type, Mx, T, E, N, K, ws, s, dev);
+        case 64: return launch_as<64>(codes, scales, x, rows, offsets, y, y_type, Mx, T, E, N, K, ws, s, dev);
+        default: return launch_as<128>(codes, scales, x, rows, offsets, y, y_type, Mx, T, E, N, K, ws, s, dev);
+    }
+}
+
+cudaError_t take_gemm_mx_error(unsigned int* out) {
+    unsigned int zero = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(out, g_gemm_mx_error, sizeof(unsigned int));
+    if (e == cudaSuccess) e = cudaMemcpyToSymbol(g_gemm_mx_error, &zero, sizeof(unsigned int));
+    return e;
+}
+
+Q4_DEFINE_TAKE_BOUNDS(mx_gemm)
+
+}  // namespace q4
