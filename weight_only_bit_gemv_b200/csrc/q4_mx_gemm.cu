@@ -51,12 +51,12 @@ namespace {
 constexpr int kThreads = 192;     // producer, MMA, four epilogue warps
 constexpr int kFlush32 = 8;       // k blocks per accumulation in tensor memory, binary32 y
 constexpr int kFlush16 = 64;      // ... bfloat16 y
-constexpr int kMinUnits = 4;      // least k blocks a CTA is started for
+constexpr int kMinBlocks = 4;     // least k blocks a CTA is started for
 constexpr uint32_t kTmemCols = 512;
 constexpr int kMaxExperts = Q4_MAX_EXPERTS;
 
 struct MxGemm {
-    const uint8_t* codes_scales;  // exponent bytes of W
+    const uint8_t* wsf;           // exponent bytes of W
     const uint8_t* xsf;           // exponent bytes of x's parts, [tile][kXBlocks][Kb][512]
     const int32_t* offsets;       // first row of each expert; nullptr: one matrix
     float* partial;               // [2 * CTAs][kTokens][128]
@@ -64,7 +64,10 @@ struct MxGemm {
     void* y;
     int64_t N;
     int64_t tile_limit;           // token tiles that the workspace holds
-    int T, E, Nb, Kb, y_bf16, flush;
+    int T, E, Nb, Kb, y_bf16;
+    int Ku;                       // units (stages) of k of a tile
+    int flush;                    // units per accumulation in tensor memory
+    int min_units;                // least units a CTA is started for
 };
 
 // Layout of the workspace, all parts multiples of 1024 bytes.
@@ -132,6 +135,54 @@ __device__ __forceinline__ uint64_t scale_desc(uint32_t saddr) {
 constexpr uint32_t mx_idesc(int N, int q) {
     return (static_cast<uint32_t>(q) << 4) | (5u << 7) | (0u << 10) | (static_cast<uint32_t>(N >> 3) << 17) |
            (1u << 23) | ((128u >> 4) << 24) | (static_cast<uint32_t>(q) << 29);
+}
+
+// One lane of a converged warp.  The producer and MMA warps run their loops
+// with all lanes, so that addresses and descriptors stay in uniform registers,
+// and only issue with one (with `if (lane == 0)` around the loop each MMA took
+// 70 cycles to issue and a stage's bookkeeping 450).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xFFFFFFFF;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r));
+    return r != 0u;
+}
+
+// mbar_wait that also gives up once another role has.
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const unsigned long long t0 = globaltimer_ns();
+    while (true) {
+        for (int i = 0; i < 64; ++i)
+            if (mbar_try_wait(bar, parity)) return true;
+        if (*abort_flag || globaltimer_ns() - t0 > kWaitLimitNs) return false;
+    }
+}
+
+// A ring's slot and the parity of its use, without divisions.
+template <int kSlots>
+struct Ring {
+    int slot = 0;
+    uint32_t parity = 0;
+    __device__ void next() {
+        if (++slot == kSlots) {
+            slot = 0;
+            parity ^= 1u;
+        }
+    }
+};
+
+// 3-D TMA load of one box into shared memory, completing on `bar`.
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2,
+                                            uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+        : "memory");
 }
 
 // Barrier of the four epilogue warps; true if `ok` was true in all of them.
@@ -363,38 +414,42 @@ template <int kTokens>
 struct Shape {
     static constexpr int kCols = 2 * kTokens;                    // MMA N
     static constexpr int kXBlocks = (kCols + kMxBlock - 1) / kMxBlock;
-    static constexpr int kABytes = kMxBlock * 128;               // codes spread over bytes
+    // k blocks of a stage: two for few tokens, whose MMAs are short beside a
+    // stage's bookkeeping
+    static constexpr int kUnit = kTokens <= 32 ? 2 : 1;
+    static constexpr int kABytes = kMxBlock * 128;               // a block's codes spread over bytes
     static constexpr int kBBytes = kCols * 128;
-    static constexpr int kStage = kABytes + kBBytes + kMxScaleBytes * (1 + kXBlocks);
+    // a stage: kUnit blocks of A, of B, A's exponents, B's (by row block, then k block)
+    static constexpr int kBAt = kUnit * kABytes;
+    static constexpr int kSfaAt = kBAt + kUnit * kBBytes;
+    static constexpr int kSfbAt = kSfaAt + kUnit * kMxScaleBytes;
+    static constexpr int kStage = kSfbAt + kUnit * kXBlocks * kMxScaleBytes;
     static constexpr int kStagePitch = (kStage + 1023) / 1024 * 1024;
-    // bytes that complete on a stage's barrier: the load that spreads the
-    // nibbles counts the bytes it reads
-    static constexpr int kTx = kMxCodeBytes + kBBytes + kMxScaleBytes * (1 + kXBlocks);
-    static constexpr int kStages = (222 * 1024 - static_cast<int>(sizeof(Table))) / kStagePitch < 12
-                                       ? (222 * 1024 - static_cast<int>(sizeof(Table))) / kStagePitch : 12;
-    static constexpr int kBuffers = 2 * kCols + 32 <= 512 ? 2 : 1;  // accumulators
+    static constexpr int kRoom = 222 * 1024 - static_cast<int>(sizeof(Table));
+    static constexpr int kStages = kRoom / kStagePitch < 12 ? kRoom / kStagePitch : 12;
+    static constexpr int kBuffers = 2 * kCols + 64 <= 512 ? 2 : 1;  // accumulators
     static constexpr uint32_t kScaleCol = kBuffers * kCols;        // two sets of exponent columns
-    static constexpr uint32_t kScaleSet = 4 * (1 + kXBlocks);
+    static constexpr uint32_t kScaleSet = 4 * kUnit * (1 + kXBlocks);
     static constexpr int kSmem = 1024 + kStages * kStagePitch + static_cast<int>(sizeof(Table)) + 512;
     static_assert(kStages >= 3, "the ring needs stages");
     static_assert(kScaleCol + 2 * kScaleSet <= kTmemCols, "tensor memory");
 };
 
-// A CTA's run of units, a unit being one k block of one output tile.
+// A CTA's run of units, a unit being kUnit k blocks of one output tile.
 // Tiles are numbered by expert, then row block of W, then token tile, so that
 // the token tiles of one row block follow each other and find its codes in L2.
 struct Segment {
-    int64_t out;            // output tile
-    int e, nb, tile, in;    // expert, row block, token tile, its number in the expert
-    int k0, k1;
+    int64_t out;          // output tile
+    int e, nb, tile, in;  // expert, row block, token tile, its number in the expert
+    int k0, k1;           // units of k
 };
 struct Runs {
     int64_t units, u, u1;
     int64_t ctas;
     __device__ Runs(const MxGemm& p, const Table& t) {
         const int64_t tiles = min(static_cast<int64_t>(t.tile[p.E]), p.tile_limit);
-        units = tiles * p.Nb * p.Kb;
-        ctas = min(static_cast<int64_t>(gridDim.x), max(units / kMinUnits, static_cast<int64_t>(1)));
+        units = tiles * p.Nb * p.Ku;
+        ctas = min(static_cast<int64_t>(gridDim.x), max(units / p.min_units, static_cast<int64_t>(1)));
         u = blockIdx.x < ctas ? start(blockIdx.x) : units;
         u1 = blockIdx.x < ctas ? start(blockIdx.x + 1) : units;
     }
@@ -403,9 +458,9 @@ struct Runs {
     __device__ int64_t owner(int64_t v) const { return ((v + 1) * ctas - 1) / units; }
     __device__ bool next(const MxGemm& p, const Table& t, Segment& s) {
         if (u >= u1) return false;
-        s.out = u / p.Kb;
-        s.k0 = static_cast<int>(u - s.out * p.Kb);
-        s.k1 = static_cast<int>(min(static_cast<int64_t>(p.Kb), s.k0 + u1 - u));
+        s.out = u / p.Ku;
+        s.k0 = static_cast<int>(u - s.out * p.Ku);
+        s.k1 = static_cast<int>(min(static_cast<int64_t>(p.Ku), s.k0 + u1 - u));
         u += s.k1 - s.k0;
         s.e = find_expert(t.tile, p.E, static_cast<int>(s.out / p.Nb));
         const int64_t local = s.out - static_cast<int64_t>(t.tile[s.e]) * p.Nb;
@@ -436,7 +491,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t words = bars + 8u * (2 * S::kStages + 5);  // tensor-memory base, abort, last arrival
     volatile uint32_t* word = reinterpret_cast<volatile uint32_t*>(smem + (words - base));
     volatile uint32_t* abort_flag = word + 1;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);
 
     if (tid == 0) {
         for (int s = 0; s < S::kStages; ++s) {
@@ -463,116 +518,142 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = *word;
 
     if (warp == 0) {
-        if (lane == 0) {
-            // ---------------------------- producer ----------------------------
-            int it = 0;
-            bool ok = true;
-            auto load_w = [&](const Segment& s, int k, int slot) {
-                const uint32_t dst = base + slot * S::kStagePitch;
-                const int64_t block = (static_cast<int64_t>(s.e) * p.Nb + s.nb) * p.Kb + k;
-                mbar_arrive_expect_tx(full(slot), S::kTx);
-                tma_load_2d(dst, &wmap, 0, static_cast<int>(block * kMxBlock), full(slot));
-                if (Q4_IN_BOUNDS(block, 1, static_cast<int64_t>(p.E) * p.Nb * p.Kb))
-                    bulk_load(dst + S::kABytes + S::kBBytes, p.codes_scales + block * kMxScaleBytes, kMxScaleBytes,
-                              full(slot));
-            };
-            auto load_x = [&](const Segment& s, int k, int slot) {
-                const uint32_t dst = base + slot * S::kStagePitch;
-                tma_load_2d(dst + S::kABytes, &xmap, k * kMxBlock, s.tile * S::kCols, full(slot));
+        // ------------------------------ producer ------------------------------
+        bool ok = true;
+        auto load_w = [&](int64_t block, int blocks, int slot) {
+            const uint32_t dst = base + slot * S::kStagePitch;
+            // the load that spreads the nibbles counts the bytes it reads
+            mbar_arrive_expect_tx(full(slot), S::kUnit * (kMxCodeBytes + S::kBBytes) +
+                                                  blocks * kMxScaleBytes * (1 + S::kXBlocks));
+            tma_load_2d(dst, &wmap, 0, static_cast<int>(block * kMxBlock), full(slot));
+            if (Q4_IN_BOUNDS(block, blocks, static_cast<int64_t>(p.E) * p.Nb * p.Kb))
+                bulk_load(dst + S::kSfaAt, p.wsf + block * kMxScaleBytes, blocks * kMxScaleBytes, full(slot));
+        };
+        auto load_x = [&](int tile, int kb, int blocks, int slot) {
+            const uint32_t dst = base + slot * S::kStagePitch;
+            tma_load_3d(dst + S::kBAt, &xmap, 0, tile * S::kCols, kb, full(slot));
 #pragma unroll
-                for (int b = 0; b < S::kXBlocks; ++b) {
-                    const int64_t at = (static_cast<int64_t>(s.tile) * S::kXBlocks + b) * p.Kb + k;
-                    if (Q4_IN_BOUNDS(at, 1, p.tile_limit * S::kXBlocks * p.Kb))
-                        bulk_load(dst + S::kABytes + S::kBBytes + kMxScaleBytes * (1 + b), p.xsf + at * kMxScaleBytes,
-                                  kMxScaleBytes, full(slot));
-                }
-            };
-            // the ring's first filling: W before the x conversion is known to be done
-            Segment s;
-            {
-                Runs runs(p, table);
-                for (int n = 0; n < S::kStages && runs.next(p, table, s);)
-                    for (int k = s.k0; k < s.k1 && n < S::kStages; ++k, ++n) load_w(s, k, n);
+            for (int b = 0; b < S::kXBlocks; ++b) {
+                const int64_t at = (static_cast<int64_t>(tile) * S::kXBlocks + b) * p.Kb + kb;
+                if (Q4_IN_BOUNDS(at, blocks, p.tile_limit * S::kXBlocks * p.Kb))
+                    bulk_load(dst + S::kSfbAt + b * S::kUnit * kMxScaleBytes, p.xsf + at * kMxScaleBytes,
+                              blocks * kMxScaleBytes, full(slot));
             }
-            pdl_wait();
-            asm volatile("fence.proxy.async;" ::: "memory");  // x's parts were written by plain stores
+        };
+        // the ring's first filling: W before the x conversion is known to be done
+        Segment s;
+        {
             Runs runs(p, table);
-            while (ok && runs.next(p, table, s)) {
-                for (int k = s.k0; k < s.k1; ++k, ++it) {
-                    const int slot = it % S::kStages;
-                    if (it >= S::kStages) {
-                        if (!mbar_wait(empty(slot), static_cast<uint32_t>(it / S::kStages - 1) & 1u) || *abort_flag) {
-                            ok = false;
-                            break;
-                        }
-                        load_w(s, k, slot);
-                    }
-                    load_x(s, k, slot);
-                }
+            for (int n = 0; n < S::kStages && runs.next(p, table, s);) {
+                const int64_t block = (static_cast<int64_t>(s.e) * p.Nb + s.nb) * p.Kb;
+                for (int k = s.k0; k < s.k1 && n < S::kStages; ++k, ++n)
+                    if (elect_one()) load_w(block + k * S::kUnit, min(S::kUnit, p.Kb - k * S::kUnit), n);
             }
-            if (!ok) {
-                atomicOr(&g_gemm_mx_error, 1u);
-                *abort_flag = 1;
-            }
-            // leave only once every copy issued has landed (bounded)
-            for (int i = it > S::kStages ? it - S::kStages : 0; i < it; ++i)
-                if (!mbar_wait(full(i % S::kStages), static_cast<uint32_t>(i / S::kStages) & 1u)) break;
         }
-        __syncwarp();
+        pdl_wait();
+        asm volatile("fence.proxy.async;" ::: "memory");  // x's parts were written by plain stores
+        Runs runs(p, table);
+        Ring<S::kStages> ring;
+        int64_t issued = 0;
+        while (ok && runs.next(p, table, s)) {
+            const int64_t block = (static_cast<int64_t>(s.e) * p.Nb + s.nb) * p.Kb;
+            for (int k = s.k0; k < s.k1; ++k) {
+                const bool first = issued < S::kStages;
+                if (!first && !wait_bar(empty(ring.slot), ring.parity ^ 1u, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                if (elect_one()) {
+                    const int kb = k * S::kUnit, blocks = min(S::kUnit, p.Kb - kb);
+                    if (!first) load_w(block + kb, blocks, ring.slot);
+                    load_x(s.tile, kb, blocks, ring.slot);
+                }
+                __syncwarp();
+                ++issued;
+                ring.next();
+            }
+        }
+        if (!ok && lane == 0) {
+            atomicOr(&g_gemm_mx_error, 1u);
+            *abort_flag = 1;
+        }
+        // leave only once every copy issued has landed (bounded)
+        for (int64_t i = issued > S::kStages ? issued - S::kStages : 0; i < issued; ++i)
+            if (!mbar_wait(full(static_cast<int>(i % S::kStages)), static_cast<uint32_t>(i / S::kStages) & 1u)) break;
     } else if (warp == 1) {
-        if (lane == 0) {
-            // ------------------------------- MMA -------------------------------
-            int it = 0, fl = 0;  // stages, accumulations
-            bool ok = true;
-            Runs runs(p, table);
-            Segment s;
-            while (ok && runs.next(p, table, s)) {
-                for (int k0 = s.k0; ok && k0 < s.k1; k0 += p.flush, ++fl) {
-                    const int buf = fl % S::kBuffers, k1 = min(s.k1, k0 + p.flush);
-                    if (fl >= S::kBuffers &&
-                        !mbar_wait(dempty(buf), static_cast<uint32_t>(fl / S::kBuffers - 1) & 1u)) {
+        // -------------------------------- MMA ---------------------------------
+        bool ok = true;
+        Runs runs(p, table);
+        Segment s;
+        Ring<S::kStages> ring;
+        Ring<S::kBuffers> dring;
+        uint32_t set = 0;
+        bool reused = false;  // the accumulator's earlier contents have to be read first
+        const uint64_t adesc = smem_desc_sw128(base, 1024), sdesc = scale_desc(base);
+        while (ok && runs.next(p, table, s)) {
+            for (int k0 = s.k0; ok && k0 < s.k1; k0 += p.flush) {
+                const int k1 = min(s.k1, k0 + p.flush);
+                if (reused && !wait_bar(dempty(dring.slot), dring.parity ^ 1u, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t d = tmem + dring.slot * S::kCols;
+                for (int k = k0; k < k1; ++k) {
+                    if (!wait_bar(full(ring.slot), ring.parity, abort_flag)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t d = tmem + buf * S::kCols;
-                    for (int k = k0; k < k1; ++k, ++it) {
-                        const int slot = it % S::kStages;
-                        if (!mbar_wait(full(slot), static_cast<uint32_t>(it / S::kStages) & 1u) || *abort_flag) {
-                            ok = false;
-                            break;
+                    if (elect_one()) {
+                        const uint32_t at = static_cast<uint32_t>(ring.slot) * (S::kStagePitch >> 4);
+                        const uint32_t sf = tmem + S::kScaleCol + set * S::kScaleSet;
+                        const int blocks = S::kUnit == 1 ? 1 : min(S::kUnit, p.Kb - k * S::kUnit);
+#pragma unroll
+                        for (int u = 0; u < S::kUnit; ++u) {
+                            if (u >= blocks) break;
+                            const uint32_t sfa = sf + 4 * u * (1 + S::kXBlocks), sfb = sfa + 4;
+                            tc_copy_scales(sfa, sdesc + at + (S::kSfaAt + u * kMxScaleBytes) / 16);
+#pragma unroll
+                            for (int b = 0; b < S::kXBlocks; ++b)
+                                tc_copy_scales(sfb + 4 * b,
+                                               sdesc + at + (S::kSfbAt + (b * S::kUnit + u) * kMxScaleBytes) / 16);
                         }
-                        tc_fence_after();
-                        const uint32_t a = base + slot * S::kStagePitch, b = a + S::kABytes, sf = b + S::kBBytes;
-                        const uint32_t sfa = tmem + S::kScaleCol + (it & 1) * S::kScaleSet, sfb = sfa + 4;
-                        tc_copy_scales(sfa, scale_desc(sf));
 #pragma unroll
-                        for (int j = 0; j < S::kXBlocks; ++j)
-                            tc_copy_scales(sfb + 4 * j, scale_desc(sf + kMxScaleBytes * (1 + j)));
-                        const uint64_t ad = smem_desc_sw128(a, 1024), bd = smem_desc_sw128(b, 1024);
+                        for (int u = 0; u < S::kUnit; ++u) {
+                            if (u >= blocks) break;
+                            const uint32_t sfa = sf + 4 * u * (1 + S::kXBlocks), sfb = sfa + 4;
 #pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            tc_mma_mx(d, ad + 2 * q, bd + 2 * q, mx_idesc(S::kCols, q), sfa, sfb,
-                                      (k > k0 || q > 0) ? 1u : 0u);
-                        tc_commit(empty(slot));
+                            for (int q = 0; q < 4; ++q)
+                                tc_mma_mx(d, adesc + at + (u * S::kABytes + 32 * q) / 16,
+                                          adesc + at + (S::kBAt + u * S::kBBytes + 32 * q) / 16,
+                                          mx_idesc(S::kCols, q), sfa, sfb, (k > k0 || u > 0 || q > 0) ? 1u : 0u);
+                        }
+                        tc_commit(empty(ring.slot));
+                        if (k == k1 - 1) tc_commit(dfull(dring.slot));
                     }
-                    if (ok) tc_commit(dfull(buf));
+                    __syncwarp();
+                    set ^= 1u;
+                    ring.next();
                 }
+                dring.next();
+                if (dring.slot == 0) reused = true;
             }
-            if (!ok) {
-                atomicOr(&g_gemm_mx_error, 2u);
-                *abort_flag = 1;
-            }
-            tc_commit(drain);
-            if (!mbar_wait(drain, 0u)) atomicOr(&g_gemm_mx_error, 4u);
         }
+        if (!ok && lane == 0) {
+            atomicOr(&g_gemm_mx_error, 2u);
+            *abort_flag = 1;
+        }
+        __syncwarp();
+        if (elect_one()) tc_commit(drain);
+        if (!mbar_wait(drain, 0u) && lane == 0) atomicOr(&g_gemm_mx_error, 4u);
         __syncwarp();
     } else {
         // ------------------------------ epilogue ------------------------------
         const int quarter = warp & 3, row = 32 * quarter + lane;
         const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * quarter) << 16);
         constexpr int kLoad = kTokens < 32 ? 8 : 32;  // columns per tensor-memory load
-        int fl = 0;
+        Ring<S::kBuffers> dring;
         bool ok = true;
         Runs runs(p, table);
         Segment s;
@@ -581,21 +662,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             float acc[kTokens];
 #pragma unroll
             for (int i = 0; i < kTokens; ++i) acc[i] = 0.0f;
-            for (int k0 = s.k0; k0 < s.k1; k0 += p.flush, ++fl) {
-                const int buf = fl % S::kBuffers;
-                if (!mbar_wait(dfull(buf), static_cast<uint32_t>(fl / S::kBuffers) & 1u) || *abort_flag) ok = false;
-                ok = __all_sync(0xFFFFFFFFu, ok);
+            for (int k0 = s.k0; k0 < s.k1; k0 += p.flush) {
+                ok = __all_sync(0xFFFFFFFFu, wait_bar(dfull(dring.slot), dring.parity, abort_flag));
                 if (!ok) break;
+                const uint32_t d = lanes + dring.slot * S::kCols;
                 tc_fence_after();
 #pragma unroll
                 for (int c = 0; c < kTokens; c += kLoad) {
                     uint32_t hi[kLoad], lo[kLoad];
                     if (kLoad == 8) {
-                        tc_ld_x8(lanes + buf * S::kCols + c, hi);
-                        tc_ld_x8(lanes + buf * S::kCols + kTokens + c, lo);
+                        tc_ld_x8(d + c, hi);
+                        tc_ld_x8(d + kTokens + c, lo);
                     } else {
-                        tc_ld_x32(lanes + buf * S::kCols + c, hi);
-                        tc_ld_x32(lanes + buf * S::kCols + kTokens + c, lo);
+                        tc_ld_x32(d + c, hi);
+                        tc_ld_x32(d + kTokens + c, lo);
                     }
                     tc_wait_ld();
 #pragma unroll
@@ -603,7 +683,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(dempty(buf));
+                if (lane == 0) mbar_arrive(dempty(dring.slot));
+                dring.next();
             }
             ok = epilogue_sync(ok);
             if (!ok) break;
@@ -619,7 +700,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 else
                     static_cast<float*>(p.y)[at] = v;
             };
-            if (s.k0 == 0 && s.k1 == p.Kb) {
+            if (s.k0 == 0 && s.k1 == p.Ku) {
 #pragma unroll
                 for (int m = 0; m < kTokens; ++m)
                     if (m < count) store(m, acc[m]);
@@ -634,8 +715,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (m < count) __stcg(mine + m * kMxBlock, acc[m]);
             __threadfence();
             epilogue_sync(true);
-            const int64_t u0 = s.out * p.Kb;
-            const int64_t c0 = runs.owner(u0), c1 = runs.owner(u0 + p.Kb - 1);
+            const int64_t u0 = s.out * p.Ku;
+            const int64_t c0 = runs.owner(u0), c1 = runs.owner(u0 + p.Ku - 1);
             if (tid == 64) word[2] = atomicAdd(p.counters + s.out, 1u) == static_cast<uint32_t>(c1 - c0) ? 1u : 0u;
             epilogue_sync(true);
             const bool last = word[2] != 0u;
@@ -704,15 +785,14 @@ cudaError_t launch_as(const uint8_t* codes, const uint8_t* scales, const uint16_
 
     CUtensorMap wmap, xmap;
     e = encode_tensor_map_2d(&wmap, codes, CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, 0,
-                             static_cast<uint64_t>(E * Nb * Kb * kMxBlock), kMxBlock, 64, kMxBlock, kMxBlock,
+                             static_cast<uint64_t>(E * Nb * Kb * kMxBlock), kMxBlock, 64, S::kUnit * kMxBlock, kMxBlock,
                              CU_TENSOR_MAP_SWIZZLE_128B);
     if (e != cudaSuccess) return e;
-    e = encode_tensor_map_2d(&xmap, c.xq, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1,
-                             static_cast<uint64_t>(l.tiles * S::kCols), static_cast<uint64_t>(Kb * kMxBlock),
-                             static_cast<uint64_t>(Kb * kMxBlock), S::kCols, 128, CU_TENSOR_MAP_SWIZZLE_128B);
+    e = encode_tensor_map_rows_by_block(&xmap, c.xq, static_cast<uint64_t>(l.tiles * S::kCols),
+                                        static_cast<uint64_t>(Kb), S::kCols, S::kUnit);
     if (e != cudaSuccess) return e;
     MxGemm p{};
-    p.codes_scales = scales;
+    p.wsf = scales;
     p.xsf = c.xsf;
     p.offsets = offsets;
     p.partial = reinterpret_cast<float*>(ws + l.partial);
@@ -725,7 +805,9 @@ cudaError_t launch_as(const uint8_t* codes, const uint8_t* scales, const uint16_
     p.Nb = static_cast<int>(Nb);
     p.Kb = c.Kb;
     p.y_bf16 = c.y_bf16;
-    p.flush = c.y_bf16 ? kFlush16 : kFlush32;
+    p.Ku = static_cast<int>((Kb + S::kUnit - 1) / S::kUnit);
+    p.flush = (c.y_bf16 ? kFlush16 : kFlush32) / S::kUnit;
+    p.min_units = kMinBlocks / S::kUnit;
     const void* fn = reinterpret_cast<const void*>(gemm_mx_kernel<kTokens>);
     constexpr int kSlot = kTokens == 8 ? 100 : kTokens == 16 ? 101 : kTokens == 32 ? 102 : kTokens == 64 ? 103 : 104;
     if (S::kSmem > dev.smem_optin) return cudaErrorNotSupported;
@@ -736,7 +818,7 @@ cudaError_t launch_as(const uint8_t* codes, const uint8_t* scales, const uint16_
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(
-        std::min(dev.sm_count, kMxMaxSms), std::max<int64_t>(1, l.tiles * Nb * Kb / kMinUnits))));
+        std::min(dev.sm_count, kMxMaxSms), std::max<int64_t>(1, l.tiles * Nb * p.Ku / p.min_units))));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = S::kSmem;
     cfg.stream = s;

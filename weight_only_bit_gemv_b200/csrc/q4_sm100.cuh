@@ -25,6 +25,12 @@ cudaError_t encode_tensor_map_2d(CUtensorMap* map, const void* base, CUtensorMap
                                  int elem_bytes, uint64_t rows, uint64_t cols, uint64_t row_bytes,
                                  uint32_t box_rows, uint32_t box_cols, CUtensorMapSwizzle swizzle);
 
+// Encodes a row-major byte matrix [rows][128 * blocks] as {128 bytes, rows,
+// blocks}, so that one box of 128 bytes x box_rows x box_blocks holds
+// box_blocks tiles of 128-byte rows, one after the other (128-byte swizzle).
+cudaError_t encode_tensor_map_rows_by_block(CUtensorMap* map, const void* base, uint64_t rows, uint64_t blocks,
+                                            uint32_t box_rows, uint32_t box_blocks);
+
 // ---------------------------------------------------------------------------
 // device
 // ---------------------------------------------------------------------------

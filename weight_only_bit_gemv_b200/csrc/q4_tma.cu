@@ -37,4 +37,18 @@ cudaError_t encode_tensor_map_2d(CUtensorMap* map, const void* base, CUtensorMap
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+cudaError_t encode_tensor_map_rows_by_block(CUtensorMap* map, const void* base, uint64_t rows, uint64_t blocks,
+                                            uint32_t box_rows, uint32_t box_blocks) {
+    std::call_once(g_once, resolve);
+    if (!g_encode) return cudaErrorNotSupported;
+    const cuuint64_t dims[3] = {128, rows, blocks};
+    const cuuint64_t strides[2] = {128 * blocks, 128};
+    const cuuint32_t box[3] = {128, box_rows, box_blocks};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 }  // namespace q4
