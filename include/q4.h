@@ -381,7 +381,8 @@ q4_status q4_dequant_mx(const uint8_t* codes, const uint8_t* scales, void* w_out
  * and partial sums.  It must not be used by anything else until the call has
  * run on the stream: calls that may overlap, recorded graphs among them, need
  * workspaces of their own.  Two launches a call.
- * Validation: Q4_ERR_SHAPE (M, T, Mx above 2^30 included), Q4_ERR_NULL,
+ * Validation: Q4_ERR_SHAPE (M, T, Mx above 2^30 included, and more than
+ * 2^31 - 1 blocks of 128 k over all tiles of y), Q4_ERR_NULL,
  * Q4_ERR_ALIGN (codes 32 bytes, all else 16), Q4_ERR_TOO_LARGE (workspace too
  * small), Q4_ERR_ARCH, Q4_ERR_CUDA.  M, T or N of 0 is valid: nothing runs.
  */

@@ -565,7 +565,7 @@ static q4_status check_rows(int64_t Mx, int64_t T, int64_t E, int64_t N, int64_t
 
 int64_t q4_gemm_experts_workspace(int64_t T, int64_t E, int64_t N, int64_t K) {
     if (check_rows(0, T, E, N, K) != Q4_OK) return -1;
-    return T == 0 || N == 0 ? 0 : static_cast<int64_t>(gemm_mx_workspace(T, E, N, K));
+    return T == 0 || N == 0 ? 0 : gemm_mx_workspace(T, E, N, K);
 }
 
 int64_t q4_gemm_mx_workspace(int64_t M, int64_t N, int64_t K) { return q4_gemm_experts_workspace(M, 1, N, K); }
@@ -579,11 +579,13 @@ static q4_status run_gemm_mx(const uint8_t* codes, const uint8_t* scales, const 
     if (y_type != Q4_F32 && y_type != Q4_BF16) return Q4_ERR_SHAPE;
     if (T == 0 || N == 0) return Q4_OK;
     if (grouped && !rows && Mx != T) return Q4_ERR_SHAPE;
+    const int64_t need = gemm_mx_workspace(T, E, N, K);
+    if (need < 0) return Q4_ERR_SHAPE;
     if (!codes || !scales || !x || !y || !workspace || (grouped && !offsets)) return Q4_ERR_NULL;
     if ((reinterpret_cast<uintptr_t>(codes) & 31u) || !aligned16(scales) || !aligned16(x) || !aligned16(rows) ||
         !aligned16(offsets) || !aligned16(y) || !aligned16(workspace))
         return Q4_ERR_ALIGN;
-    if (workspace_bytes < static_cast<int64_t>(gemm_mx_workspace(T, E, N, K))) return Q4_ERR_TOO_LARGE;
+    if (workspace_bytes < need) return Q4_ERR_TOO_LARGE;
     DeviceInfo dev;
     if ((st = gate(&dev)) != Q4_OK) return st;
     return after_launch(

@@ -63,7 +63,7 @@ struct MxGemm {
     uint32_t* counters;           // [tiles]
     void* y;
     int64_t N;
-    int64_t tile_limit;           // token tiles that the workspace holds
+    int tile_limit;               // token tiles that the workspace holds
     int T, E, Nb, Kb, y_bf16;
     int Ku;                       // units (stages) of k of a tile
     int flush;                    // units per accumulation in tensor memory
@@ -439,38 +439,68 @@ struct Shape {
 // Tiles are numbered by expert, then row block of W, then token tile, so that
 // the token tiles of one row block follow each other and find its codes in L2.
 struct Segment {
-    int64_t out;          // output tile
+    int out;              // output tile
     int e, nb, tile, in;  // expert, row block, token tile, its number in the expert
     int k0, k1;           // units of k
 };
+// All counts fit 31 bits (the API refuses more units than that).
 struct Runs {
-    int64_t units, u, u1;
-    int64_t ctas;
+    int units, ctas, each, more, u, u1;  // CTAs below `more` take one unit beyond `each`
     __device__ Runs(const MxGemm& p, const Table& t) {
-        const int64_t tiles = min(static_cast<int64_t>(t.tile[p.E]), p.tile_limit);
-        units = tiles * p.Nb * p.Ku;
-        ctas = min(static_cast<int64_t>(gridDim.x), max(units / p.min_units, static_cast<int64_t>(1)));
-        u = blockIdx.x < ctas ? start(blockIdx.x) : units;
-        u1 = blockIdx.x < ctas ? start(blockIdx.x + 1) : units;
+        units = min(t.tile[p.E], p.tile_limit) * p.Nb * p.Ku;
+        ctas = min(static_cast<int>(gridDim.x), max(units / p.min_units, 1));
+        each = units / ctas;
+        more = units - each * ctas;
+        const int c = blockIdx.x;
+        u = c < ctas ? start(c) : units;
+        u1 = c < ctas ? start(c + 1) : units;
     }
-    __device__ int64_t start(int64_t c) const { return units * c / ctas; }
+    __device__ int start(int c) const { return each * c + min(c, more); }
     // the CTA whose run holds unit v
-    __device__ int64_t owner(int64_t v) const { return ((v + 1) * ctas - 1) / units; }
+    __device__ int owner(int v) const {
+        const int longer = more * (each + 1);
+        return v < longer ? v / (each + 1) : more + (v - longer) / each;
+    }
     __device__ bool next(const MxGemm& p, const Table& t, Segment& s) {
         if (u >= u1) return false;
         s.out = u / p.Ku;
-        s.k0 = static_cast<int>(u - s.out * p.Ku);
-        s.k1 = static_cast<int>(min(static_cast<int64_t>(p.Ku), s.k0 + u1 - u));
+        s.k0 = u - s.out * p.Ku;
+        s.k1 = min(p.Ku, s.k0 + u1 - u);
         u += s.k1 - s.k0;
-        s.e = find_expert(t.tile, p.E, static_cast<int>(s.out / p.Nb));
-        const int64_t local = s.out - static_cast<int64_t>(t.tile[s.e]) * p.Nb;
-        const int mine = t.tile[s.e + 1] - t.tile[s.e];
-        s.nb = static_cast<int>(local / mine);
-        s.in = static_cast<int>(local % mine);
+        s.e = p.E == 1 ? 0 : find_expert(t.tile, p.E, s.out / p.Nb);
+        const int local = s.out - t.tile[s.e] * p.Nb, mine = t.tile[s.e + 1] - t.tile[s.e];
+        s.nb = mine == 1 ? local : local / mine;
+        s.in = local - s.nb * mine;
         s.tile = t.tile[s.e] + s.in;
         return true;
     }
 };
+
+// Four consecutive outputs n .. n + 3 of row `at` / N.
+__device__ __forceinline__ void store4(const MxGemm& p, int64_t at, int64_t n, const float4& v) {
+    const float f[4] = {v.x, v.y, v.z, v.w};
+    if ((p.N & 3) == 0) {  // then rows are aligned for it
+        if (n >= p.N || !Q4_IN_BOUNDS(at, 4, static_cast<int64_t>(p.T) * p.N)) return;
+        if (p.y_bf16) {
+            const __nv_bfloat162 a = __floats2bfloat162_rn(f[0], f[1]), b = __floats2bfloat162_rn(f[2], f[3]);
+            uint2 w;
+            w.x = *reinterpret_cast<const uint32_t*>(&a);
+            w.y = *reinterpret_cast<const uint32_t*>(&b);
+            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.y) + at) = w;
+        } else {
+            *reinterpret_cast<float4*>(static_cast<float*>(p.y) + at) = v;
+        }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (n + i >= p.N || !Q4_IN_BOUNDS(at + i, 1, static_cast<int64_t>(p.T) * p.N)) continue;
+        if (p.y_bf16)
+            static_cast<__nv_bfloat16*>(p.y)[at + i] = __float2bfloat16_rn(f[i]);
+        else
+            static_cast<float*>(p.y)[at + i] = f[i];
+    }
+}
 
 template <int kTokens>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -535,7 +565,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int b = 0; b < S::kXBlocks; ++b) {
                 const int64_t at = (static_cast<int64_t>(tile) * S::kXBlocks + b) * p.Kb + kb;
-                if (Q4_IN_BOUNDS(at, blocks, p.tile_limit * S::kXBlocks * p.Kb))
+                if (Q4_IN_BOUNDS(at, blocks, static_cast<int64_t>(p.tile_limit) * S::kXBlocks * p.Kb))
                     bulk_load(dst + S::kSfbAt + b * S::kUnit * kMxScaleBytes, p.xsf + at * kMxScaleBytes,
                               blocks * kMxScaleBytes, full(slot));
             }
@@ -708,31 +738,47 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             // A part of a tile.  A run that begins inside the tile owns slot
             // 2 c, one that begins with it (or before) slot 2 c + 1.
-            auto slot_of = [&](int64_t c, bool inside) { return p.partial + ((2 * c + (inside ? 0 : 1)) * kTokens) * kMxBlock + row; };
-            float* mine = slot_of(blockIdx.x, s.k0 > 0);
+            auto slot_of = [&](int c, bool inside) {
+                return p.partial + static_cast<int64_t>(2 * c + (inside ? 0 : 1)) * kTokens * kMxBlock;
+            };
+            float* mine = slot_of(blockIdx.x, s.k0 > 0) + row;
 #pragma unroll
             for (int m = 0; m < kTokens; ++m)
                 if (m < count) __stcg(mine + m * kMxBlock, acc[m]);
             __threadfence();
             epilogue_sync(true);
-            const int64_t u0 = s.out * p.Ku;
-            const int64_t c0 = runs.owner(u0), c1 = runs.owner(u0 + p.Ku - 1);
+            const int u0 = s.out * p.Ku, c0 = runs.owner(u0), c1 = runs.owner(u0 + p.Ku - 1);
             if (tid == 64) word[2] = atomicAdd(p.counters + s.out, 1u) == static_cast<uint32_t>(c1 - c0) ? 1u : 0u;
             epilogue_sync(true);
-            const bool last = word[2] != 0u;
-            if (!last) continue;
+            if (word[2] == 0u) continue;
             __threadfence();
+            // each warp adds up every fourth token, four rows of W a lane,
+            // with kBatch tokens' loads of a part in flight
+            constexpr int kBatch = kTokens / 4 < 8 ? kTokens / 4 : 8;
+            const int64_t n4 = static_cast<int64_t>(s.nb) * kMxBlock + 4 * lane;
+            for (int m0 = warp - 2; m0 < count; m0 += 4 * kBatch) {
+                float4 sum[kBatch];
 #pragma unroll
-            for (int i = 0; i < kTokens; ++i) acc[i] = 0.0f;
-            for (int64_t c = c0; c <= c1; ++c) {
-                const float* part = slot_of(c, runs.start(c) > u0);
+                for (int b = 0; b < kBatch; ++b) sum[b] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 2
+                for (int c = c0; c <= c1; ++c) {
+                    const float* part = slot_of(c, runs.start(c) > u0) + 4 * lane;
+                    float4 v[kBatch];
 #pragma unroll
-                for (int m = 0; m < kTokens; ++m)
-                    if (m < count) acc[m] += __ldcg(part + m * kMxBlock);
+                    for (int b = 0; b < kBatch; ++b)
+                        v[b] = __ldcg(reinterpret_cast<const float4*>(part + min(m0 + 4 * b, count - 1) * kMxBlock));
+#pragma unroll
+                    for (int b = 0; b < kBatch; ++b) {
+                        sum[b].x += v[b].x;
+                        sum[b].y += v[b].y;
+                        sum[b].z += v[b].z;
+                        sum[b].w += v[b].w;
+                    }
+                }
+#pragma unroll
+                for (int b = 0; b < kBatch; ++b)
+                    if (m0 + 4 * b < count) store4(p, static_cast<int64_t>(first + m0 + 4 * b) * p.N + n4, n4, sum[b]);
             }
-#pragma unroll
-            for (int m = 0; m < kTokens; ++m)
-                if (m < count) store(m, acc[m]);
         }
         if (!ok && lane == 0) {
             atomicOr(&g_gemm_mx_error, 8u);
@@ -799,7 +845,7 @@ cudaError_t launch_as(const uint8_t* codes, const uint8_t* scales, const uint16_
     p.counters = c.counters;
     p.y = y;
     p.N = N;
-    p.tile_limit = l.tiles;
+    p.tile_limit = static_cast<int>(l.tiles);
     p.T = c.T;
     p.E = c.E;
     p.Nb = static_cast<int>(Nb);
@@ -829,8 +875,10 @@ cudaError_t launch_as(const uint8_t* codes, const uint8_t* scales, const uint16_
 
 }  // namespace
 
-size_t gemm_mx_workspace(int64_t T, int64_t E, int64_t N, int64_t K) {
-    return workspace_layout(T, E, N, K, tokens_per_tile(T, E)).bytes;
+int64_t gemm_mx_workspace(int64_t T, int64_t E, int64_t N, int64_t K) {
+    const Workspace l = workspace_layout(T, E, N, K, tokens_per_tile(T, E));
+    if (l.tiles > INT32_MAX / (mx_blocks(N) * mx_blocks(K))) return -1;
+    return static_cast<int64_t>(l.bytes);
 }
 
 cudaError_t launch_gemm_mx(const uint8_t* codes, const uint8_t* scales, const uint16_t* x, const int32_t* rows,
