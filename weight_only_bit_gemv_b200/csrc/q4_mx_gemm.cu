@@ -54,17 +54,20 @@ constexpr int kFlush16 = 64;      // ... bfloat16 y
 constexpr int kMinBlocks = 4;     // least k blocks a CTA is started for
 constexpr uint32_t kTmemCols = 512;
 constexpr int kMaxExperts = Q4_MAX_EXPERTS;
+constexpr int kPairTokens = 120;  // most tokens of a pair's tile: two accumulators of 240 columns
 
 struct MxGemm {
     const uint8_t* wsf;           // exponent bytes of W
-    const uint8_t* xsf;           // exponent bytes of x's parts, [tile][kXBlocks][Kb][512]
+    const uint8_t* xsf;           // exponent bytes of x's parts, [tile][x_blocks][Kb][512]
     const int32_t* offsets;       // first row of each expert; nullptr: one matrix
-    float* partial;               // [2 * CTAs][kTokens][128]
-    uint32_t* counters;           // [tiles]
+    float* partial;               // [2 * CTAs][tokens][128]
+    uint32_t* counters;           // one for each 128 rows of an output tile
     void* y;
     int64_t N;
     int tile_limit;               // token tiles that the workspace holds
     int T, E, Nb, Kb, y_bf16;
+    int tokens;                   // of a tile
+    int Nt;                       // row tiles of W: Nb, or pairs of row blocks
     int Ku;                       // units (stages) of k of a tile
     int flush;                    // units per accumulation in tensor memory
     int min_units;                // least units a CTA is started for
@@ -76,27 +79,35 @@ struct Workspace {
     size_t counters, xq, xsf, partial, bytes;
 };
 
-int x_blocks(int tokens) { return (2 * tokens + kMxBlock - 1) / kMxBlock; }
+// Blocks of 128 columns (x rows, hi and lo) whose exponents a tile has.
+int x_blocks(int tokens, bool pair) { return pair ? 2 : (2 * tokens + kMxBlock - 1) / kMxBlock; }
 
-// Tokens per tile: the smallest tile that holds an expert's average share.
-// (Measured rule; see the table of tile sizes beside the launcher.)
-int tokens_per_tile(int64_t T, int64_t E) {
+// Up to 64 tokens an expert: the smallest tile of 8, 16, 32, 64 that holds an
+// expert's average share.  More: pairs of CTAs, and the share in equal tiles of
+// at most 120 tokens.
+struct Plan {
+    int tokens;
+    bool pair;
+};
+Plan plan_for(int64_t T, int64_t E) {
     const int64_t share = (T + E - 1) / E;
-    for (int t = 8; t < 128; t *= 2)
-        if (share <= t) return t;
-    return 128;
+    for (int t = 8; t <= 64; t *= 2)
+        if (share <= t) return {t, false};
+    const int64_t tiles = (share + kPairTokens - 1) / kPairTokens;
+    return {static_cast<int>(((share + tiles - 1) / tiles + 7) / 8 * 8), true};
 }
 
-Workspace workspace_layout(int64_t T, int64_t E, int64_t N, int64_t K, int tokens) {
+Workspace workspace_layout(int64_t T, int64_t E, int64_t N, int64_t K, const Plan& plan) {
     auto up = [](size_t n) { return (n + 1023) / 1024 * 1024; };
     const int64_t Nb = mx_blocks(N), Kb = mx_blocks(K);
+    const int tokens = plan.tokens;
     Workspace w{};
     // an expert with c > 0 rows has at most c / tokens + 1 tiles
     w.tiles = E == 1 ? (T + tokens - 1) / tokens : std::min(T, T / tokens + E);
     w.counters = 0;
-    w.xq = up(static_cast<size_t>(w.tiles) * Nb * sizeof(uint32_t));
+    w.xq = up(static_cast<size_t>(w.tiles) * (Nb + 1) * sizeof(uint32_t));
     w.xsf = w.xq + up(static_cast<size_t>(w.tiles) * 2 * tokens * Kb * kMxBlock);
-    w.partial = w.xsf + up(static_cast<size_t>(w.tiles) * x_blocks(tokens) * Kb * kMxScaleBytes);
+    w.partial = w.xsf + up(static_cast<size_t>(w.tiles) * x_blocks(tokens, plan.pair) * Kb * kMxScaleBytes);
     w.bytes = w.partial + up(static_cast<size_t>(2) * kMxMaxSms * tokens * kMxBlock * sizeof(float));
     return w;
 }
@@ -107,20 +118,100 @@ Workspace workspace_layout(int64_t T, int64_t E, int64_t N, int64_t K, int token
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
+// tcgen05 instructions of one CTA (kCtas = 1) or of a pair (2): one thread of
+// the pair's first CTA then acts for both, each CTA's own shared and tensor
+// memory at the same addresses.
+#define Q4_TC(one, two, ...)                  \
+    do {                                      \
+        if constexpr (kCtas == 1)             \
+            asm volatile(one __VA_ARGS__);    \
+        else                                  \
+            asm volatile(two __VA_ARGS__);    \
+    } while (0)
+
 // 512 exponent bytes from shared memory to four columns of tensor memory,
 // repeated in the four lane quarters.
+template <int kCtas>
 __device__ __forceinline__ void tc_copy_scales(uint32_t taddr, uint64_t desc) {
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+    Q4_TC("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;", "tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;",
+          ::"r"(taddr), "l"(desc) : "memory");
 }
 
 // D[tmem] (+)= (A * sfa) x (B * sfb)^T, both operands in shared memory.
+template <int kCtas>
 __device__ __forceinline__ void tc_mma_mx(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
                                           uint32_t sfb, uint32_t accumulate) {
+    Q4_TC("{\n\t.reg .pred p;\n\t"
+          "setp.ne.b32 p, %6, 0;\n\t"
+          "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}",
+          "{\n\t.reg .pred p;\n\t"
+          "setp.ne.b32 p, %6, 0;\n\t"
+          "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}",
+          ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate) : "memory");
+}
+
+// One arrival on `bar`, in every CTA of the group, when all prior MMAs and
+// copies of this thread are complete.
+template <int kCtas>
+__device__ __forceinline__ void tc_commit_all(uint32_t bar) {
+    if constexpr (kCtas == 1)
+        tc_commit(bar);
+    else
+        asm volatile(
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+            "h"(static_cast<uint16_t>(3))
+            : "memory");
+}
+template <int kCtas>
+__device__ __forceinline__ void tc_commit_own(uint32_t bar) {
+    Q4_TC("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];",
+          "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];", ::"r"(bar) : "memory");
+}
+template <int kCtas>
+__device__ __forceinline__ void tmem_alloc_all(uint32_t dst) {
+    Q4_TC("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;",
+          "tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;", ::"r"(dst), "r"(kTmemCols) : "memory");
+    Q4_TC("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;",
+          "tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;", ::: "memory");
+}
+template <int kCtas>
+__device__ __forceinline__ void tmem_free_all(uint32_t taddr) {
+    Q4_TC("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;", "tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;",
+          ::"r"(taddr), "r"(kTmemCols) : "memory");
+}
+#undef Q4_TC
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm("mov.u32 %0, %cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The address in the pair's first CTA of what is at `addr` in this one.
+__device__ __forceinline__ uint32_t in_first_cta(uint32_t addr) {
+    uint32_t a;
+    asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(addr));
+    return a;
+}
+__device__ __forceinline__ void arrive_cluster(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// TMA loads into this CTA that complete on a barrier of either CTA of the pair.
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap* map, int c0, int c1, uint32_t bar) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2,
+                                                 uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
         : "memory");
 }
 
@@ -130,11 +221,11 @@ __device__ __forceinline__ uint64_t scale_desc(uint32_t saddr) {
            (1ull << 46);
 }
 
-// Instruction descriptor: A e2m1, B e4m3, power-of-two scales, M = 128; the
-// scale byte q of each 32-bit column is taken on both sides.
-constexpr uint32_t mx_idesc(int N, int q) {
+// Instruction descriptor: A e2m1, B e4m3, power-of-two scales; the scale byte
+// q of each 32-bit column is taken on both sides.
+__host__ __device__ constexpr uint32_t mx_idesc(int M, int N, int q) {
     return (static_cast<uint32_t>(q) << 4) | (5u << 7) | (0u << 10) | (static_cast<uint32_t>(N >> 3) << 17) |
-           (1u << 23) | ((128u >> 4) << 24) | (static_cast<uint32_t>(q) << 29);
+           (1u << 23) | (static_cast<uint32_t>(M >> 4) << 24) | (static_cast<uint32_t>(q) << 29);
 }
 
 // One lane of a converged warp.  The producer and MMA warps run their loops
@@ -208,14 +299,13 @@ struct Table {
     int tile[kMaxExperts + 1];
 };
 
-template <int kTokens>
-__device__ void fill_table(Table& t, const int32_t* __restrict__ offsets, int E, int T) {
+__device__ void fill_table(Table& t, const int32_t* __restrict__ offsets, int E, int T, int tokens) {
     if (!offsets) {
         if (threadIdx.x == 0) {
             t.offset[0] = 0;
             t.offset[1] = T;
             t.tile[0] = 0;
-            t.tile[1] = (T + kTokens - 1) / kTokens;
+            t.tile[1] = (T + tokens - 1) / tokens;
         }
     } else if (threadIdx.x < 32) {
         const int lane = threadIdx.x;
@@ -235,7 +325,7 @@ __device__ void fill_table(Table& t, const int32_t* __restrict__ offsets, int E,
             const int before = max(high, lane ? up : 0);
             first = max(first, before);
             last = max(last, first);
-            const int mine = e < E ? (last - first + kTokens - 1) / kTokens : 0;
+            const int mine = e < E ? (last - first + tokens - 1) / tokens : 0;
             int sum = mine;
 #pragma unroll
             for (int d = 1; d < 32; d *= 2) {
@@ -294,16 +384,15 @@ struct Convert {
     uint32_t* counters;
     void* y;
     int64_t Mx, K, N, counter_count, tile_limit;
-    int T, E, Kb, y_bf16;
+    int T, E, Kb, y_bf16, tokens, x_blocks;
 };
 
 // One warp converts 256 k of one row: 4 lanes a group of 32, 8 values a lane.
-template <int kTokens, bool kVector>
+template <bool kVector>
 __global__ void __launch_bounds__(256) convert_kernel(const Convert p) {
-    constexpr int kXBlocks = (2 * kTokens + kMxBlock - 1) / kMxBlock;
     __shared__ Table table;
     pdl_launch();
-    fill_table<kTokens>(table, p.offsets, p.E, p.T);
+    fill_table(table, p.offsets, p.E, p.T, p.tokens);
     const int64_t thread = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x;
     const int64_t threads = static_cast<int64_t>(gridDim.x) * blockDim.x;
     for (int64_t i = thread; i < p.counter_count; i += threads) p.counters[i] = 0;
@@ -323,9 +412,9 @@ __global__ void __launch_bounds__(256) convert_kernel(const Convert p) {
         const int row = static_cast<int>(job / pieces), piece = static_cast<int>(job % pieces);
         const int e = find_expert(table.offset, p.E, row);
         const int in = row - table.offset[e];
-        const int64_t tile = table.tile[e] + in / kTokens;
+        const int64_t tile = table.tile[e] + in / p.tokens;
         if (row < table.offset[0] || tile >= p.tile_limit) continue;  // offsets that do not start at 0
-        const int m = in % kTokens;
+        const int m = in % p.tokens;
         const int64_t src = p.rows ? static_cast<int64_t>(__ldg(p.rows + row)) : row;
         const bool have = src >= 0 && src < p.Mx;
         const int64_t k = piece * 256 + 8 * lane;
@@ -376,11 +465,11 @@ __global__ void __launch_bounds__(256) convert_kernel(const Convert p) {
         }
         if (kb < p.Kb) {
             const int64_t Kp = static_cast<int64_t>(p.Kb) * kMxBlock;
-            [[maybe_unused]] const int64_t extent = p.tile_limit * 2 * kTokens * Kp;
-            const int64_t at = (tile * 2 * kTokens + m) * Kp + k;
-            if (Q4_IN_BOUNDS(at, 8, extent) && Q4_IN_BOUNDS(at + kTokens * Kp, 8, extent)) {
+            [[maybe_unused]] const int64_t extent = p.tile_limit * 2 * p.tokens * Kp;
+            const int64_t at = (tile * 2 * p.tokens + m) * Kp + k;
+            if (Q4_IN_BOUNDS(at, 8, extent) && Q4_IN_BOUNDS(at + p.tokens * Kp, 8, extent)) {
                 *reinterpret_cast<uint2*>(p.xq + at) = hi;
-                *reinterpret_cast<uint2*>(p.xq + at + kTokens * Kp) = lo;
+                *reinterpret_cast<uint2*>(p.xq + at + p.tokens * Kp) = lo;
             }
         }
         // the four groups of a k block: one 32-bit store per part.  A group
@@ -394,11 +483,11 @@ __global__ void __launch_bounds__(256) convert_kernel(const Convert p) {
             four_lo |= (b == 255u ? 255u : b - 5u) << (8 * g);
         }
         if ((lane & 15) == 0 && kb < p.Kb) {
-            [[maybe_unused]] const int64_t extent = p.tile_limit * kXBlocks * p.Kb * kMxScaleBytes;
-            const int r = kTokens + m;
-            const int64_t at = ((tile * kXBlocks + m / kMxBlock) * p.Kb + kb) * kMxScaleBytes + mx_scale_at(m % kMxBlock, 0);
+            [[maybe_unused]] const int64_t extent = p.tile_limit * p.x_blocks * p.Kb * kMxScaleBytes;
+            const int r = p.tokens + m;
+            const int64_t at = ((tile * p.x_blocks + m / kMxBlock) * p.Kb + kb) * kMxScaleBytes + mx_scale_at(m % kMxBlock, 0);
             const int64_t at_lo =
-                ((tile * kXBlocks + r / kMxBlock) * p.Kb + kb) * kMxScaleBytes + mx_scale_at(r % kMxBlock, 0);
+                ((tile * p.x_blocks + r / kMxBlock) * p.Kb + kb) * kMxScaleBytes + mx_scale_at(r % kMxBlock, 0);
             if (Q4_IN_BOUNDS(at, 4, extent) && Q4_IN_BOUNDS(at_lo, 4, extent)) {
                 *reinterpret_cast<uint32_t*>(p.xsf + at) = four;
                 *reinterpret_cast<uint32_t*>(p.xsf + at_lo) = four_lo;
@@ -410,7 +499,11 @@ __global__ void __launch_bounds__(256) convert_kernel(const Convert p) {
 // ---------------------------------------------------------------------------
 // the product
 // ---------------------------------------------------------------------------
-template <int kTokens>
+// kTokens: of a tile, or for a pair (kCtas = 2) the most a tile may have.  A
+// pair's MMA has 256 rows of W, 128 in each CTA, and reads its columns from
+// both: the first CTA holds the hi rows of x, the second the lo rows, so each
+// byte of x is brought to one SM for 256 rows of W.
+template <int kTokens, int kCtas>
 struct Shape {
     static constexpr int kCols = 2 * kTokens;                    // MMA N
     static constexpr int kXBlocks = (kCols + kMxBlock - 1) / kMxBlock;
@@ -418,7 +511,7 @@ struct Shape {
     // stage's bookkeeping
     static constexpr int kUnit = kTokens <= 32 ? 2 : 1;
     static constexpr int kABytes = kMxBlock * 128;               // a block's codes spread over bytes
-    static constexpr int kBBytes = kCols * 128;
+    static constexpr int kBBytes = kCols / kCtas * 128;
     // a stage: kUnit blocks of A, of B, A's exponents, B's (by row block, then k block)
     static constexpr int kBAt = kUnit * kABytes;
     static constexpr int kSfaAt = kBAt + kUnit * kBBytes;
@@ -427,31 +520,29 @@ struct Shape {
     static constexpr int kStagePitch = (kStage + 1023) / 1024 * 1024;
     static constexpr int kRoom = 222 * 1024 - static_cast<int>(sizeof(Table));
     static constexpr int kStages = kRoom / kStagePitch < 12 ? kRoom / kStagePitch : 12;
-    static constexpr int kBuffers = 2 * kCols + 64 <= 512 ? 2 : 1;  // accumulators
-    static constexpr uint32_t kScaleCol = kBuffers * kCols;        // two sets of exponent columns
     static constexpr uint32_t kScaleSet = 4 * kUnit * (1 + kXBlocks);
+    static constexpr uint32_t kScaleCol = 2 * kCols;               // after two accumulators, two sets of exponents
     static constexpr int kSmem = 1024 + kStages * kStagePitch + static_cast<int>(sizeof(Table)) + 512;
     static_assert(kStages >= 3, "the ring needs stages");
     static_assert(kScaleCol + 2 * kScaleSet <= kTmemCols, "tensor memory");
 };
 
-// A CTA's run of units, a unit being kUnit k blocks of one output tile.
-// Tiles are numbered by expert, then row block of W, then token tile, so that
-// the token tiles of one row block follow each other and find its codes in L2.
+// The run of units of a CTA or pair, a unit being kUnit k blocks of one output tile.
+// Tiles are numbered by expert, then rows of W, then token tile, so that the
+// token tiles of the same rows follow each other and find their codes in L2.
 struct Segment {
     int out;              // output tile
-    int e, nb, tile, in;  // expert, row block, token tile, its number in the expert
+    int e, nt, tile, in;  // expert, row tile, token tile, its number in the expert
     int k0, k1;           // units of k
 };
 // All counts fit 31 bits (the API refuses more units than that).
 struct Runs {
     int units, ctas, each, more, u, u1;  // CTAs below `more` take one unit beyond `each`
-    __device__ Runs(const MxGemm& p, const Table& t) {
-        units = min(t.tile[p.E], p.tile_limit) * p.Nb * p.Ku;
-        ctas = min(static_cast<int>(gridDim.x), max(units / p.min_units, 1));
+    __device__ Runs(const MxGemm& p, const Table& t, int c, int groups) {
+        units = min(t.tile[p.E], p.tile_limit) * p.Nt * p.Ku;
+        ctas = min(groups, max(units / p.min_units, 1));
         each = units / ctas;
         more = units - each * ctas;
-        const int c = blockIdx.x;
         u = c < ctas ? start(c) : units;
         u1 = c < ctas ? start(c + 1) : units;
     }
@@ -467,10 +558,10 @@ struct Runs {
         s.k0 = u - s.out * p.Ku;
         s.k1 = min(p.Ku, s.k0 + u1 - u);
         u += s.k1 - s.k0;
-        s.e = p.E == 1 ? 0 : find_expert(t.tile, p.E, s.out / p.Nb);
-        const int local = s.out - t.tile[s.e] * p.Nb, mine = t.tile[s.e + 1] - t.tile[s.e];
-        s.nb = mine == 1 ? local : local / mine;
-        s.in = local - s.nb * mine;
+        s.e = p.E == 1 ? 0 : find_expert(t.tile, p.E, s.out / p.Nt);
+        const int local = s.out - t.tile[s.e] * p.Nt, mine = t.tile[s.e + 1] - t.tile[s.e];
+        s.nt = mine == 1 ? local : local / mine;
+        s.in = local - s.nt * mine;
         s.tile = t.tile[s.e] + s.in;
         return true;
     }
@@ -502,11 +593,15 @@ __device__ __forceinline__ void store4(const MxGemm& p, int64_t at, int64_t n, c
     }
 }
 
-template <int kTokens>
+template <int kTokens, int kCtas>
 __global__ void __launch_bounds__(kThreads, 1)
     gemm_mx_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
+                   const __grid_constant__ CUtensorMap wsfmap, const __grid_constant__ CUtensorMap xsfmap,
                    const MxGemm p) {
-    using S = Shape<kTokens>;
+    using S = Shape<kTokens, kCtas>;
+    const int tokens = kCtas == 1 ? kTokens : p.tokens;
+    const uint32_t rank = kCtas == 1 ? 0u : cluster_rank();
+    const int group = blockIdx.x / kCtas, groups = gridDim.x / kCtas;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
     uint8_t* smem = smem_raw + (base - smem_u32(smem_raw));
@@ -530,7 +625,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(dfull(b), 1);
-            mbar_init(dempty(b), 4);
+            mbar_init(dempty(b), 4 * kCtas);
         }
         mbar_init(drain, 1);
         *abort_flag = 0;
@@ -539,54 +634,74 @@ __global__ void __launch_bounds__(kThreads, 1)
         prefetch_tensor_map(&xmap);
     }
     if (warp == 1) {
-        tmem_alloc(words, kTmemCols);
-        tmem_relinquish();
+        tmem_alloc_all<kCtas>(words);
     }
     tc_fence_before();
-    fill_table<kTokens>(table, p.offsets, p.E, p.T);  // ends in __syncthreads
+    fill_table(table, p.offsets, p.E, p.T, tokens);  // ends in __syncthreads
+    if (kCtas > 1) cluster_sync();                   // the other CTA's barriers exist
     tc_fence_after();
     const uint32_t tmem = *word;
 
     if (warp == 0) {
         // ------------------------------ producer ------------------------------
         bool ok = true;
+        // A pair's loads all complete on the first CTA's barrier, which expects
+        // the bytes of both (a count of bytes may run ahead of that).
+        const uint32_t leader_full = kCtas == 1 ? bars : in_first_cta(bars);
         auto load_w = [&](int64_t block, int blocks, int slot) {
-            const uint32_t dst = base + slot * S::kStagePitch;
+            const uint32_t dst = base + slot * S::kStagePitch, bar = leader_full + 8u * slot;
             // the load that spreads the nibbles counts the bytes it reads
-            mbar_arrive_expect_tx(full(slot), S::kUnit * (kMxCodeBytes + S::kBBytes) +
-                                                  blocks * kMxScaleBytes * (1 + S::kXBlocks));
-            tma_load_2d(dst, &wmap, 0, static_cast<int>(block * kMxBlock), full(slot));
+            const int brows = kCtas == 1 ? S::kCols : tokens;
+            if (rank == 0)
+                mbar_arrive_expect_tx(full(slot), kCtas * (S::kUnit * (kMxCodeBytes + brows * 128) +
+                                                           blocks * kMxScaleBytes * (1 + S::kXBlocks)));
+            if (kCtas > 1) {
+                tma_load_2d_pair(dst, &wmap, 0, static_cast<int>(block * kMxBlock), bar);
+                tma_load_2d_pair(dst + S::kSfaAt, &wsfmap, 0, static_cast<int>(block), bar);
+                return;
+            }
+            tma_load_2d(dst, &wmap, 0, static_cast<int>(block * kMxBlock), bar);
             if (Q4_IN_BOUNDS(block, blocks, static_cast<int64_t>(p.E) * p.Nb * p.Kb))
-                bulk_load(dst + S::kSfaAt, p.wsf + block * kMxScaleBytes, blocks * kMxScaleBytes, full(slot));
+                bulk_load(dst + S::kSfaAt, p.wsf + block * kMxScaleBytes, blocks * kMxScaleBytes, bar);
         };
         auto load_x = [&](int tile, int kb, int blocks, int slot) {
-            const uint32_t dst = base + slot * S::kStagePitch;
-            tma_load_3d(dst + S::kBAt, &xmap, 0, tile * S::kCols, kb, full(slot));
+            const uint32_t dst = base + slot * S::kStagePitch, bar = leader_full + 8u * slot;
+            if (kCtas > 1) {
+                tma_load_3d_pair(dst + S::kBAt, &xmap, 0, (2 * tile + static_cast<int>(rank)) * tokens, kb, bar);
+#pragma unroll
+                for (int b = 0; b < S::kXBlocks; ++b)
+                    tma_load_2d_pair(dst + S::kSfbAt + b * kMxScaleBytes, &xsfmap, 0,
+                                     (tile * S::kXBlocks + b) * p.Kb + kb, bar);
+                return;
+            }
+            tma_load_3d(dst + S::kBAt, &xmap, 0, tile * S::kCols, kb, bar);
 #pragma unroll
             for (int b = 0; b < S::kXBlocks; ++b) {
                 const int64_t at = (static_cast<int64_t>(tile) * S::kXBlocks + b) * p.Kb + kb;
                 if (Q4_IN_BOUNDS(at, blocks, static_cast<int64_t>(p.tile_limit) * S::kXBlocks * p.Kb))
                     bulk_load(dst + S::kSfbAt + b * S::kUnit * kMxScaleBytes, p.xsf + at * kMxScaleBytes,
-                              blocks * kMxScaleBytes, full(slot));
+                              blocks * kMxScaleBytes, bar);
             }
         };
+        // a pair's second CTA without rows of its own reads the first's
+        auto row_block = [&](const Segment& s) { return min(s.nt * kCtas + static_cast<int>(rank), p.Nb - 1); };
         // the ring's first filling: W before the x conversion is known to be done
         Segment s;
         {
-            Runs runs(p, table);
+            Runs runs(p, table, group, groups);
             for (int n = 0; n < S::kStages && runs.next(p, table, s);) {
-                const int64_t block = (static_cast<int64_t>(s.e) * p.Nb + s.nb) * p.Kb;
+                const int64_t block = (static_cast<int64_t>(s.e) * p.Nb + row_block(s)) * p.Kb;
                 for (int k = s.k0; k < s.k1 && n < S::kStages; ++k, ++n)
                     if (elect_one()) load_w(block + k * S::kUnit, min(S::kUnit, p.Kb - k * S::kUnit), n);
             }
         }
         pdl_wait();
         asm volatile("fence.proxy.async;" ::: "memory");  // x's parts were written by plain stores
-        Runs runs(p, table);
+        Runs runs(p, table, group, groups);
         Ring<S::kStages> ring;
         int64_t issued = 0;
         while (ok && runs.next(p, table, s)) {
-            const int64_t block = (static_cast<int64_t>(s.e) * p.Nb + s.nb) * p.Kb;
+            const int64_t block = (static_cast<int64_t>(s.e) * p.Nb + row_block(s)) * p.Kb;
             for (int k = s.k0; k < s.k1; ++k) {
                 const bool first = issued < S::kStages;
                 if (!first && !wait_bar(empty(ring.slot), ring.parity ^ 1u, abort_flag)) {
@@ -607,19 +722,23 @@ __global__ void __launch_bounds__(kThreads, 1)
             atomicOr(&g_gemm_mx_error, 1u);
             *abort_flag = 1;
         }
-        // leave only once every copy issued has landed (bounded)
-        for (int64_t i = issued > S::kStages ? issued - S::kStages : 0; i < issued; ++i)
+        // leave only once every copy issued has landed (bounded); a pair's
+        // second CTA leaves after the first, at the cluster's barrier below
+        for (int64_t i = rank != 0 ? issued : issued > S::kStages ? issued - S::kStages : 0; i < issued; ++i)
             if (!mbar_wait(full(static_cast<int>(i % S::kStages)), static_cast<uint32_t>(i / S::kStages) & 1u)) break;
+    } else if (warp == 1 && rank != 0) {
+        // the pair's first CTA issues for both
     } else if (warp == 1) {
         // -------------------------------- MMA ---------------------------------
         bool ok = true;
-        Runs runs(p, table);
+        Runs runs(p, table, group, groups);
         Segment s;
         Ring<S::kStages> ring;
-        Ring<S::kBuffers> dring;
+        Ring<2> dring;
         uint32_t set = 0;
         bool reused = false;  // the accumulator's earlier contents have to be read first
         const uint64_t adesc = smem_desc_sw128(base, 1024), sdesc = scale_desc(base);
+        const uint32_t idesc = mx_idesc(kMxBlock * kCtas, 2 * tokens, 0);
         while (ok && runs.next(p, table, s)) {
             for (int k0 = s.k0; ok && k0 < s.k1; k0 += p.flush) {
                 const int k1 = min(s.k1, k0 + p.flush);
@@ -643,10 +762,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int u = 0; u < S::kUnit; ++u) {
                             if (u >= blocks) break;
                             const uint32_t sfa = sf + 4 * u * (1 + S::kXBlocks), sfb = sfa + 4;
-                            tc_copy_scales(sfa, sdesc + at + (S::kSfaAt + u * kMxScaleBytes) / 16);
+                            tc_copy_scales<kCtas>(sfa, sdesc + at + (S::kSfaAt + u * kMxScaleBytes) / 16);
 #pragma unroll
                             for (int b = 0; b < S::kXBlocks; ++b)
-                                tc_copy_scales(sfb + 4 * b,
+                                tc_copy_scales<kCtas>(sfb + 4 * b,
                                                sdesc + at + (S::kSfbAt + (b * S::kUnit + u) * kMxScaleBytes) / 16);
                         }
 #pragma unroll
@@ -655,12 +774,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                             const uint32_t sfa = sf + 4 * u * (1 + S::kXBlocks), sfb = sfa + 4;
 #pragma unroll
                             for (int q = 0; q < 4; ++q)
-                                tc_mma_mx(d, adesc + at + (u * S::kABytes + 32 * q) / 16,
+                                tc_mma_mx<kCtas>(d, adesc + at + (u * S::kABytes + 32 * q) / 16,
                                           adesc + at + (S::kBAt + u * S::kBBytes + 32 * q) / 16,
-                                          mx_idesc(S::kCols, q), sfa, sfb, (k > k0 || u > 0 || q > 0) ? 1u : 0u);
+                                          idesc | mx_idesc(0, 0, q), sfa, sfb, (k > k0 || u > 0 || q > 0) ? 1u : 0u);
                         }
-                        tc_commit(empty(ring.slot));
-                        if (k == k1 - 1) tc_commit(dfull(dring.slot));
+                        tc_commit_all<kCtas>(empty(ring.slot));
+                        if (k == k1 - 1) tc_commit_all<kCtas>(dfull(dring.slot));
                     }
                     __syncwarp();
                     set ^= 1u;
@@ -675,17 +794,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             *abort_flag = 1;
         }
         __syncwarp();
-        if (elect_one()) tc_commit(drain);
+        if (elect_one()) tc_commit_own<kCtas>(drain);
         if (!mbar_wait(drain, 0u) && lane == 0) atomicOr(&g_gemm_mx_error, 4u);
         __syncwarp();
     } else {
         // ------------------------------ epilogue ------------------------------
         const int quarter = warp & 3, row = 32 * quarter + lane;
         const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * quarter) << 16);
-        constexpr int kLoad = kTokens < 32 ? 8 : 32;  // columns per tensor-memory load
-        Ring<S::kBuffers> dring;
+        constexpr int kLoad = kTokens % 32 == 0 ? 32 : 8;                    // columns of a tensor-memory load
+        constexpr int kWait = kTokens % 24 == 0 ? 24 : kTokens < 32 ? kTokens : 32;  // ... of a wait for them
+        Ring<2> dring;
         bool ok = true;
-        Runs runs(p, table);
+        Runs runs(p, table, group, groups);
         Segment s;
         pdl_wait();  // the counters' zeros, and whoever read the workspace before
         while (ok && runs.next(p, table, s)) {
@@ -698,29 +818,44 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t d = lanes + dring.slot * S::kCols;
                 tc_fence_after();
 #pragma unroll
-                for (int c = 0; c < kTokens; c += kLoad) {
-                    uint32_t hi[kLoad], lo[kLoad];
-                    if (kLoad == 8) {
-                        tc_ld_x8(d + c, hi);
-                        tc_ld_x8(d + kTokens + c, lo);
-                    } else {
-                        tc_ld_x32(d + c, hi);
-                        tc_ld_x32(d + kTokens + c, lo);
+                for (int c0 = 0; c0 < kTokens; c0 += kWait) {
+                    if (c0 >= tokens) break;
+                    uint32_t hi[kWait], lo[kWait];
+#pragma unroll
+                    for (int c = 0; c < kWait; c += kLoad) {
+                        if (c0 + c >= tokens) break;
+                        if constexpr (kLoad == 8) {
+                            tc_ld_x8(d + c0 + c, hi + c);
+                            tc_ld_x8(d + tokens + c0 + c, lo + c);
+                        } else {
+                            tc_ld_x32(d + c0 + c, hi + c);
+                            tc_ld_x32(d + tokens + c0 + c, lo + c);
+                        }
                     }
                     tc_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < kLoad; ++i) acc[c + i] += __uint_as_float(hi[i]) + __uint_as_float(lo[i]);
+                    for (int c = 0; c < kWait; c += kLoad) {
+                        if (c0 + c >= tokens) break;
+#pragma unroll
+                        for (int i = 0; i < kLoad; ++i)
+                            acc[c0 + c + i] += __uint_as_float(hi[c + i]) + __uint_as_float(lo[c + i]);
+                    }
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(dempty(dring.slot));
+                if (lane == 0) {
+                    if (rank == 0)
+                        mbar_arrive(dempty(dring.slot));
+                    else
+                        arrive_cluster(in_first_cta(dempty(dring.slot)));
+                }
                 dring.next();
             }
             ok = epilogue_sync(ok);
             if (!ok) break;
-            const int first = table.offset[s.e] + s.in * kTokens;
-            const int count = min(kTokens, table.offset[s.e + 1] - first);
-            const int64_t n = static_cast<int64_t>(s.nb) * kMxBlock + row;
+            const int first = table.offset[s.e] + s.in * tokens;
+            const int count = min(tokens, table.offset[s.e + 1] - first);
+            const int64_t n0 = (static_cast<int64_t>(s.nt) * kCtas + rank) * kMxBlock, n = n0 + row;
             [[maybe_unused]] const int64_t yextent = static_cast<int64_t>(p.T) * p.N;
             auto store = [&](int m, float v) {
                 const int64_t at = static_cast<int64_t>(first + m) * p.N + n;
@@ -739,23 +874,23 @@ __global__ void __launch_bounds__(kThreads, 1)
             // A part of a tile.  A run that begins inside the tile owns slot
             // 2 c, one that begins with it (or before) slot 2 c + 1.
             auto slot_of = [&](int c, bool inside) {
-                return p.partial + static_cast<int64_t>(2 * c + (inside ? 0 : 1)) * kTokens * kMxBlock;
+                return p.partial + static_cast<int64_t>((2 * c + (inside ? 0 : 1)) * kCtas + static_cast<int>(rank)) * tokens * kMxBlock;
             };
-            float* mine = slot_of(blockIdx.x, s.k0 > 0) + row;
+            float* mine = slot_of(group, s.k0 > 0) + row;
 #pragma unroll
             for (int m = 0; m < kTokens; ++m)
                 if (m < count) __stcg(mine + m * kMxBlock, acc[m]);
             __threadfence();
             epilogue_sync(true);
             const int u0 = s.out * p.Ku, c0 = runs.owner(u0), c1 = runs.owner(u0 + p.Ku - 1);
-            if (tid == 64) word[2] = atomicAdd(p.counters + s.out, 1u) == static_cast<uint32_t>(c1 - c0) ? 1u : 0u;
+            if (tid == 64) word[2] = atomicAdd(p.counters + s.out * kCtas + rank, 1u) == static_cast<uint32_t>(c1 - c0) ? 1u : 0u;
             epilogue_sync(true);
             if (word[2] == 0u) continue;
             __threadfence();
             // each warp adds up every fourth token, four rows of W a lane,
             // with kBatch tokens' loads of a part in flight
             constexpr int kBatch = kTokens / 4 < 8 ? kTokens / 4 : 8;
-            const int64_t n4 = static_cast<int64_t>(s.nb) * kMxBlock + 4 * lane;
+            const int64_t n4 = n0 + 4 * lane;
             for (int m0 = warp - 2; m0 < count; m0 += 4 * kBatch) {
                 float4 sum[kBatch];
 #pragma unroll
@@ -790,18 +925,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     pdl_wait();  // no CTA ends before the conversion has: it writes y's last rows
     tc_fence_before();
     __syncthreads();
+    if (kCtas > 1) cluster_sync();  // neither CTA's memory goes while the other may use it
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc(tmem, kTmemCols);
+        tmem_free_all<kCtas>(tmem);
     }
 }
 
-template <int kTokens>
-cudaError_t launch_as(const uint8_t* codes, const uint8_t* scales, const uint16_t* x, const int32_t* rows,
+template <int kTokens, int kCtas>
+cudaError_t launch_as(const Plan& plan, const uint8_t* codes, const uint8_t* scales, const uint16_t* x, const int32_t* rows,
                       const int32_t* offsets, void* y, int y_type, int64_t Mx, int64_t T, int64_t E, int64_t N,
                       int64_t K, uint8_t* ws, cudaStream_t s, const DeviceInfo& dev) {
-    using S = Shape<kTokens>;
-    const Workspace l = workspace_layout(T, E, N, K, kTokens);
+    using S = Shape<kTokens, kCtas>;
+    const Workspace l = workspace_layout(T, E, N, K, plan);
     const int64_t Nb = mx_blocks(N), Kb = mx_blocks(K);
     Convert c{};
     c.x = x;
@@ -814,29 +950,41 @@ cudaError_t launch_as(const uint8_t* codes, const uint8_t* scales, const uint16_
     c.Mx = Mx;
     c.K = K;
     c.N = N;
-    c.counter_count = l.tiles * Nb;
+    c.counter_count = l.tiles * (Nb + 1);
     c.tile_limit = l.tiles;
     c.T = static_cast<int>(T);
     c.E = static_cast<int>(E);
     c.Kb = static_cast<int>(Kb);
     c.y_bf16 = y_type == Q4_BF16;
+    c.tokens = plan.tokens;
+    c.x_blocks = x_blocks(plan.tokens, plan.pair);
     const int64_t warps = std::max(T * ((Kb + 1) / 2), (c.counter_count + 255) / 256);
     const int grid = static_cast<int>(std::min<int64_t>((warps + 7) / 8, dev.sm_count * 8));
     if (K % 8 == 0)
-        convert_kernel<kTokens, true><<<grid, 256, 0, s>>>(c);
+        convert_kernel<true><<<grid, 256, 0, s>>>(c);
     else
-        convert_kernel<kTokens, false><<<grid, 256, 0, s>>>(c);
+        convert_kernel<false><<<grid, 256, 0, s>>>(c);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
 
-    CUtensorMap wmap, xmap;
+    CUtensorMap wmap, xmap, wsfmap, xsfmap;
     e = encode_tensor_map_2d(&wmap, codes, CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, 0,
                              static_cast<uint64_t>(E * Nb * Kb * kMxBlock), kMxBlock, 64, S::kUnit * kMxBlock, kMxBlock,
                              CU_TENSOR_MAP_SWIZZLE_128B);
     if (e != cudaSuccess) return e;
-    e = encode_tensor_map_rows_by_block(&xmap, c.xq, static_cast<uint64_t>(l.tiles * S::kCols),
-                                        static_cast<uint64_t>(Kb), S::kCols, S::kUnit);
+    e = encode_tensor_map_rows_by_block(&xmap, c.xq, static_cast<uint64_t>(l.tiles * 2 * plan.tokens),
+                                        static_cast<uint64_t>(Kb), 2 * plan.tokens / kCtas, S::kUnit);
     if (e != cudaSuccess) return e;
+    wsfmap = xsfmap = wmap;  // not used by one CTA, which copies exponents without a map
+    if (kCtas > 1) {
+        const uint64_t x_rows = static_cast<uint64_t>(l.tiles) * c.x_blocks * Kb;
+        e = encode_tensor_map_2d(&wsfmap, scales, CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, static_cast<uint64_t>(E * Nb * Kb),
+                                 128, kMxScaleBytes, 1, 128, CU_TENSOR_MAP_SWIZZLE_NONE);
+        if (e == cudaSuccess)
+            e = encode_tensor_map_2d(&xsfmap, c.xsf, CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, x_rows, 128, kMxScaleBytes, 1,
+                                     128, CU_TENSOR_MAP_SWIZZLE_NONE);
+        if (e != cudaSuccess) return e;
+    }
     MxGemm p{};
     p.wsf = scales;
     p.xsf = c.xsf;
@@ -850,33 +998,39 @@ cudaError_t launch_as(const uint8_t* codes, const uint8_t* scales, const uint16_
     p.E = c.E;
     p.Nb = static_cast<int>(Nb);
     p.Kb = c.Kb;
+    p.tokens = plan.tokens;
+    p.Nt = static_cast<int>((Nb + kCtas - 1) / kCtas);
     p.y_bf16 = c.y_bf16;
     p.Ku = static_cast<int>((Kb + S::kUnit - 1) / S::kUnit);
     p.flush = (c.y_bf16 ? kFlush16 : kFlush32) / S::kUnit;
     p.min_units = kMinBlocks / S::kUnit;
-    const void* fn = reinterpret_cast<const void*>(gemm_mx_kernel<kTokens>);
+    const void* fn = reinterpret_cast<const void*>(gemm_mx_kernel<kTokens, kCtas>);
     constexpr int kSlot = kTokens == 8 ? 100 : kTokens == 16 ? 101 : kTokens == 32 ? 102 : kTokens == 64 ? 103 : 104;
     if (S::kSmem > dev.smem_optin) return cudaErrorNotSupported;
     e = ensure_smem_attr(fn, S::kSmem, kSlot, dev.device);
     if (e != cudaSuccess) return e;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = kCtas;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(
-        std::min(dev.sm_count, kMxMaxSms), std::max<int64_t>(1, l.tiles * Nb * p.Ku / p.min_units))));
+    const int64_t groups = std::min<int64_t>(std::min(dev.sm_count, kMxMaxSms) / kCtas,
+                                             std::max<int64_t>(1, l.tiles * p.Nt * p.Ku / p.min_units));
+    cfg.gridDim = dim3(static_cast<unsigned>(groups * kCtas));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = S::kSmem;
     cfg.stream = s;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, gemm_mx_kernel<kTokens>, wmap, xmap, p);
+    cfg.numAttrs = kCtas == 1 ? 1 : 2;
+    return cudaLaunchKernelEx(&cfg, gemm_mx_kernel<kTokens, kCtas>, wmap, xmap, wsfmap, xsfmap, p);
 }
 
 }  // namespace
 
 int64_t gemm_mx_workspace(int64_t T, int64_t E, int64_t N, int64_t K) {
-    const Workspace l = workspace_layout(T, E, N, K, tokens_per_tile(T, E));
+    const Workspace l = workspace_layout(T, E, N, K, plan_for(T, E));
     if (l.tiles > INT32_MAX / (mx_blocks(N) * mx_blocks(K))) return -1;
     return static_cast<int64_t>(l.bytes);
 }
@@ -885,13 +1039,12 @@ cudaError_t launch_gemm_mx(const uint8_t* codes, const uint8_t* scales, const ui
                            const int32_t* offsets, void* y, int y_type, int64_t Mx, int64_t T, int64_t E, int64_t N,
                            int64_t K, void* workspace, cudaStream_t s, const DeviceInfo& dev) {
     uint8_t* ws = static_cast<uint8_t*>(workspace);
-    switch (tokens_per_tile(T, E)) {
-        case 8: return launch_as<8>(codes, scales, x, rows, offsets, y, y_type, Mx, T, E, N, K, ws, s, dev);
-        case 16: return launch_as<16>(codes, scales, x, rows, offsets, y, y_type, Mx, T, E, N, K, ws, s, dev);
-        case 32: return launch_as<32>(codes, scales, x, rows, offsets, y, y_type, Mx, T, E, N, K, ws, s, dev);
-        case 64: return launch_as<64>(codes, scales, x, rows, offsets, y, y_type, Mx, T, E, N, K, ws, s, dev);
-        default: return launch_as<128>(codes, scales, x, rows, offsets, y, y_type, Mx, T, E, N, K, ws, s, dev);
-    }
+    const Plan plan = plan_for(T, E);
+    const auto launch = plan.pair           ? launch_as<kPairTokens, 2>
+                        : plan.tokens == 8  ? launch_as<8, 1>
+                        : plan.tokens == 16 ? launch_as<16, 1>
+                        : plan.tokens == 32 ? launch_as<32, 1> : launch_as<64, 1>;
+    return launch(plan, codes, scales, x, rows, offsets, y, y_type, Mx, T, E, N, K, ws, s, dev);
 }
 
 cudaError_t take_gemm_mx_error(unsigned int* out) {
