@@ -567,6 +567,22 @@ struct Runs {
     }
 };
 
+// acc[0 .. count) to `out` and every N-th element behind it.  (Short on
+// purpose: with the address and the bounds worked out for each token, 120
+// unrolled stores were so much code that a tile's took 14 us.)
+template <int kTokens, typename T>
+__device__ __forceinline__ void store_column(T* out, int64_t N, const float (&acc)[kTokens], int count) {
+#pragma unroll
+    for (int m0 = 0; m0 < kTokens; m0 += 8) {
+        if (m0 >= count) break;
+#pragma unroll
+        for (int m = m0; m < m0 + 8; ++m) {
+            if (m < count) *out = Element<T>::put(acc[m]);
+            out += N;
+        }
+    }
+}
+
 // Four consecutive outputs n .. n + 3 of row `at` / N.
 __device__ __forceinline__ void store4(const MxGemm& p, int64_t at, int64_t n, const float4& v) {
     const float f[4] = {v.x, v.y, v.z, v.w};
@@ -856,19 +872,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int first = table.offset[s.e] + s.in * tokens;
             const int count = min(tokens, table.offset[s.e + 1] - first);
             const int64_t n0 = (static_cast<int64_t>(s.nt) * kCtas + rank) * kMxBlock, n = n0 + row;
-            [[maybe_unused]] const int64_t yextent = static_cast<int64_t>(p.T) * p.N;
-            auto store = [&](int m, float v) {
-                const int64_t at = static_cast<int64_t>(first + m) * p.N + n;
-                if (n >= p.N || !Q4_IN_BOUNDS(at, 1, yextent)) return;
-                if (p.y_bf16)
-                    static_cast<__nv_bfloat16*>(p.y)[at] = __float2bfloat16_rn(v);
-                else
-                    static_cast<float*>(p.y)[at] = v;
-            };
             if (s.k0 == 0 && s.k1 == p.Ku) {
-#pragma unroll
-                for (int m = 0; m < kTokens; ++m)
-                    if (m < count) store(m, acc[m]);
+                // one row of W a thread: a warp's store is 32 outputs of a token in a row
+                const int64_t at = static_cast<int64_t>(first) * p.N + n;
+                if (n < p.N && Q4_IN_BOUNDS(at + (count - 1) * p.N, 1, static_cast<int64_t>(p.T) * p.N)) {
+                    if (p.y_bf16)
+                        store_column<kTokens>(static_cast<__nv_bfloat16*>(p.y) + at, p.N, acc, count);
+                    else
+                        store_column<kTokens>(static_cast<float*>(p.y) + at, p.N, acc, count);
+                }
                 continue;
             }
             // A part of a tile.  A run that begins inside the tile owns slot
