@@ -377,10 +377,13 @@ q4_status q4_dequant_mx(const uint8_t* codes, const uint8_t* scales, void* w_out
  * nothing.  E <= Q4_MAX_EXPERTS.
  *
  * Both use the caller's workspace (16-byte aligned, any contents, q4_gemm_mx_
- * workspace / q4_gemm_experts_workspace bytes; -1 for bad sizes) for x's parts
- * and partial sums.  It must not be used by anything else until the call has
+ * workspace / q4_gemm_experts_workspace bytes; -1 for bad sizes, 0 where none
+ * is needed, at few tokens, and NULL will do) for x's parts and partial sums.
+ * It must not be used by anything else until the call has
  * run on the stream: calls that may overlap, recorded graphs among them, need
- * workspaces of their own.  Two launches a call.
+ * workspaces of their own.  Two launches a call, one at few tokens, which may
+ * start before the preceding kernel on the stream has ended but reads nothing
+ * before that (programmatic dependent launch).
  * Validation: Q4_ERR_SHAPE (M, T, Mx above 2^30 included, and more than
  * 2^31 - 1 blocks of 128 k over all tiles of y), Q4_ERR_NULL,
  * Q4_ERR_ALIGN (codes 32 bytes, all else 16), Q4_ERR_TOO_LARGE (workspace too

@@ -28,16 +28,15 @@ def _f64(t):
     return t.detach().double().cpu().numpy()
 
 
-def _packed(rng, N, K, E=None, spread=0.05):
-    """Random packed matrices, on the GPU and as 64-bit values."""
-    w = [rng.standard_normal((N, K)) * spread * 2.0 ** rng.integers(-3, 4, (N, 1)) for _ in range(E or 1)]
-    packed = [ref.pack(v) for v in w]
-    codes = torch.from_numpy(np.stack([p[0] for p in packed]))
-    scales = torch.from_numpy(np.stack([p[1] for p in packed]))
-    values = [ref.unpack(*p, N, K) for p in packed]
-    if E is None:
-        return codes[0].cuda(), scales[0].cuda(), values[0]
-    return codes.cuda(), scales.cuda(), values
+def _packed(rng, N, K, E=None):
+    """Random packed matrices, on the GPU and as 64-bit values: every code, and
+    a spread of scales."""
+    nb, kb = -(-N // 128), -(-K // 128)
+    codes = rng.integers(0, 256, (E or 1, nb, kb, 128, 64), dtype=np.uint8)
+    scales = rng.integers(118, 125, (E or 1, nb, kb, 512), dtype=np.uint8)
+    values = [ref.unpack(c, s, N, K) for c, s in zip(codes, scales)]
+    codes, scales = torch.from_numpy(codes).cuda(), torch.from_numpy(scales).cuda()
+    return (codes[0], scales[0], values[0]) if E is None else (codes, scales, values)
 
 
 def _x(rng, M, K, spread=1.0):
@@ -153,6 +152,18 @@ def test_gemm_long_and_wide(M, N, K):
     _close(q4.q4_gemm_mx(codes, scales, x, N=N, dtype=torch.bfloat16), w, x)
 
 
+@pytest.mark.parametrize("M", [1, 3, 8])
+@pytest.mark.parametrize("N,K", [(128, 3000), (130, 1500), (5000, 1408), (4096, 4096), (128, 11008), (20000, 2304), (18900, 4224)])
+def test_gemm_few_tokens(M, N, K):
+    """Every split of K over a tile's thread blocks, rings that go round many
+    times, one tile and several for a block, and K of an odd number of blocks."""
+    rng = np.random.default_rng(M + N + K)
+    codes, scales, w = _packed(rng, N, K)
+    for _ in range(3):
+        x = _x(rng, M, K)
+        _close(q4.q4_gemm_mx(codes, scales, x, N=N), w, x)
+
+
 @pytest.mark.parametrize("M", [1, 5, 16, 31, 64, 130])
 def test_gemm_exact_on_integers(M):
     """Whole-number x and scales of 1: every sum is a multiple of 1/2 below
@@ -240,9 +251,10 @@ def test_gemm_outputs_workspace_and_stream(M):
     by_handle = q4.q4_gemm_mx(codes, scales, x, N=N, stream=side.cuda_stream)
     side.synchronize()
     assert torch.equal(by_handle, want)
-    with pytest.raises(q4.Q4Error) as e:
-        q4.q4_gemm_mx(codes, scales, x, N=N, workspace=ws[:need - 16])
-    assert e.value.status == 6
+    if need > 0:                                               # few tokens need none
+        with pytest.raises(q4.Q4Error) as e:
+            q4.q4_gemm_mx(codes, scales, x, N=N, workspace=ws[:need - 16])
+        assert e.value.status == 6
 
 
 def test_gemm_in_graphs():

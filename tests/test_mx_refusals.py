@@ -45,7 +45,7 @@ def test_pack_and_dequant(lib, name):
 
 
 def test_gemm(lib):
-    def f(codes=A, scales=A, x=A, y=A, type_=0, M=4, N=64, K=96, ws=A, bytes_=BIG):
+    def f(codes=A, scales=A, x=A, y=A, type_=0, M=40, N=64, K=96, ws=A, bytes_=BIG):
         return lib.q4_gemm_mx(codes, scales, x, y, type_, M, N, K, ws, bytes_, None)
     assert f(M=-1) == SHAPE
     assert f(N=-1) == SHAPE
@@ -59,7 +59,7 @@ def test_gemm(lib):
         assert f(**{name: None}) == NULL
         assert f(**{name: MIS}) == ALIGN
     assert f(codes=HALF) == ALIGN
-    need = lib.q4_gemm_mx_workspace(4, 64, 96)
+    need = lib.q4_gemm_mx_workspace(40, 64, 96)
     assert need > 0 and f(bytes_=need - 1) == TOO_LARGE
     assert lib.q4_gemm_mx_workspace(-1, 64, 96) == -1
     assert lib.q4_gemm_mx_workspace(4, 64, 0) == -1
@@ -67,7 +67,7 @@ def test_gemm(lib):
 
 
 def test_gemm_experts(lib):
-    def f(codes=A, scales=A, x=A, rows=A, offsets=A, y=A, type_=1, Mx=4, T=8, E=3, N=64, K=96, ws=A, bytes_=BIG):
+    def f(codes=A, scales=A, x=A, rows=A, offsets=A, y=A, type_=1, Mx=4, T=80, E=3, N=64, K=96, ws=A, bytes_=BIG):
         return lib.q4_gemm_experts(codes, scales, x, rows, offsets, y, type_, Mx, T, E, N, K, ws, bytes_, None)
     assert f(E=0) == SHAPE
     assert f(E=1025) == SHAPE
@@ -75,13 +75,13 @@ def test_gemm_experts(lib):
     assert f(Mx=-1) == SHAPE
     assert f(T=(1 << 30) + 1) == SHAPE
     assert f(rows=None) == SHAPE                             # then x has T rows
-    assert f(rows=None, Mx=8, offsets=None) == NULL
+    assert f(rows=None, Mx=80, offsets=None) == NULL
     assert f(T=0, codes=None) == OK
     for name in ("codes", "scales", "x", "offsets", "y", "ws"):
         assert f(**{name: None}) == NULL
     for name in ("codes", "scales", "x", "rows", "offsets", "y", "ws"):
         assert f(**{name: MIS}) == ALIGN
-    need = lib.q4_gemm_experts_workspace(8, 3, 64, 96)
+    need = lib.q4_gemm_experts_workspace(80, 3, 64, 96)
     assert need > 0 and f(bytes_=need - 1) == TOO_LARGE
     assert lib.q4_gemm_experts_workspace(8, 1025, 64, 96) == -1
 

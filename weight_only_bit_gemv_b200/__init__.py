@@ -27,6 +27,7 @@ allocate belongs to the stream that they run on.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import re
@@ -356,42 +357,47 @@ MX_GROUP = 32
 _TYPE = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 
 
-class _On:
-    """The device, stream and allocations of one call: the tensors' device is
-    made current, and what the call allocates belongs to the stream that it
-    runs on, so that it can be freed before the call has run."""
+class _Foreign:
+    """The context of a call on another stream or device than the current one:
+    makes the tensors' device current, and what the call allocates belong to
+    the stream that it runs on, so that it can be freed before the call has run."""
 
-    __slots__ = ("device", "stream", "_guards")
+    __slots__ = ("_guards",)
 
-    def __init__(self, t: torch.Tensor, stream):
-        self.device = t.device
-        index = t.device.index
-        self._guards = ()
-        if stream is None:
-            self.stream = torch._C._cuda_getCurrentRawStream(index)
-            if index != torch.cuda.current_device():
-                self._guards = (torch.cuda.device(index),)
-        else:
-            self.stream = int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
-            owner = stream if hasattr(stream, "cuda_stream") else \
-                torch.cuda.ExternalStream(self.stream, device=t.device)
-            self._guards = (torch.cuda.device(index), torch.cuda.stream(owner))
+    def __init__(self, index: int, stream):
+        self._guards = [torch.cuda.device(index)]
+        if stream is not None:
+            if not hasattr(stream, "cuda_stream"):
+                stream = torch.cuda.ExternalStream(int(stream), device=torch.device("cuda", index))
+            self._guards.append(torch.cuda.stream(stream))
 
     def __enter__(self):
         for g in self._guards:
             g.__enter__()
-        return self
 
     def __exit__(self, *exc):
         for g in reversed(self._guards):
             g.__exit__(*exc)
 
-    def empty(self, shape, dtype) -> torch.Tensor:
-        return torch.empty(shape, dtype=dtype, device=self.device)
+
+_HERE_ALREADY = contextlib.nullcontext()
+
+
+def _on(t: torch.Tensor, stream):
+    """(stream handle, context) of a call on ``t``'s device and ``stream``, the
+    device's current one if None."""
+    index = t.get_device()
+    if stream is not None:
+        return int(getattr(stream, "cuda_stream", stream)), _Foreign(index, stream)
+    return (torch._C._cuda_getCurrentRawStream(index),
+            _HERE_ALREADY if index == torch._C._cuda_getDevice() else _Foreign(index, None))
 
 
 def _operand(t, name: str, dtypes, shape, on: torch.Tensor) -> None:
     """One tensor of a call: its type, shape, layout and device."""
+    if (isinstance(t, torch.Tensor) and t.dtype in dtypes and t.shape == shape and t.is_cuda
+            and t.get_device() == on.get_device() and t.is_contiguous()):
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype not in dtypes:
@@ -402,8 +408,7 @@ def _operand(t, name: str, dtypes, shape, on: torch.Tensor) -> None:
         raise ValueError(f"{name} must be a CUDA tensor")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if t.device != on.device:
-        raise ValueError(f"{name} is on {t.device}, not on {on.device}")
+    raise ValueError(f"{name} is on {t.device}, not on {on.device}")
 
 
 def _dims(t, name: str, dims, form: str) -> None:
@@ -450,17 +455,18 @@ def q4_pack_mx(w: torch.Tensor, codes: torch.Tensor = None, scales: torch.Tensor
     lead = tuple(w.shape[:-2])
     nb, kb = -(-N // MX_BLOCK), -(-K // MX_BLOCK)
     _operand(w, "w", _FLOATS, w.shape, w)
-    with _On(w, stream) as on:
+    handle, context = _on(w, stream)
+    with context:
         if codes is None:
-            codes = on.empty((*lead, nb, kb, MX_BLOCK, MX_BLOCK // 2), torch.uint8)
+            codes = torch.empty((*lead, nb, kb, MX_BLOCK, MX_BLOCK // 2), dtype=torch.uint8, device=w.device)
         else:
             _operand(codes, "codes", _BYTES, (*lead, nb, kb, MX_BLOCK, MX_BLOCK // 2), w)
         if scales is None:
-            scales = on.empty((*lead, nb, kb, 512), torch.uint8)
+            scales = torch.empty((*lead, nb, kb, 512), dtype=torch.uint8, device=w.device)
         else:
             _operand(scales, "scales", _BYTES, (*lead, nb, kb, 512), w)
         st = load().q4_pack_mx(w.data_ptr(), _TYPE[w.dtype], codes.data_ptr(), scales.data_ptr(),
-                               lead[0] if lead else 1, N, K, on.stream)
+                               lead[0] if lead else 1, N, K, handle)
     _check(st, "q4_pack_mx")
     return codes, scales
 
@@ -471,35 +477,41 @@ def q4_dequant_mx(codes: torch.Tensor, scales: torch.Tensor, w_out: torch.Tensor
     ``dtype``.  N and K default to whole blocks."""
     E, N, K = _mx_sizes(codes, scales, N, K)
     shape = (N, K) if E is None else (E, N, K)
-    with _On(codes, stream) as on:
+    handle, context = _on(codes, stream)
+    with context:
         if w_out is None:
             _type(dtype, _FLOATS, "dtype")
-            w_out = on.empty(shape, dtype)
+            w_out = torch.empty(shape, dtype=dtype, device=codes.device)
         else:
             _operand(w_out, "w_out", _FLOATS, shape, codes)
         st = load().q4_dequant_mx(codes.data_ptr(), scales.data_ptr(), w_out.data_ptr(),
-                                  _TYPE[w_out.dtype], 1 if E is None else E, N, K, on.stream)
+                                  _TYPE[w_out.dtype], 1 if E is None else E, N, K, handle)
     _check(st, "q4_dequant_mx")
     return w_out
 
 
-def _scratch(on, workspace, need: int, of: torch.Tensor, what: str):
-    """A call's workspace: the caller's, or one of the call's own."""
+def _scratch(workspace, need: int, of: torch.Tensor, what: str):
+    """(address, bytes) of a call's workspace and the tensor that holds it: the
+    caller's, or one of the call's own."""
     if need < 0:
         _check(2, what)
     if workspace is None:
-        return on.empty(need, torch.uint8)
+        if need == 0:
+            return None, 0, None
+        workspace = torch.empty(need, dtype=torch.uint8, device=of.device)
+        return workspace.data_ptr(), need, workspace
+    _dims(workspace, "workspace", (1,), "[bytes]")
     _operand(workspace, "workspace", _BYTES, workspace.shape, of)
-    return workspace
+    return workspace.data_ptr(), workspace.numel(), workspace
 
 
 def q4_gemm_mx_workspace(M: int, N: int, K: int) -> int:
-    """Bytes of workspace that q4_gemm_mx needs (-1 for sizes it refuses)."""
+    """Bytes of workspace that q4_gemm_mx needs (0: none, -1: it refuses the sizes)."""
     return int(load().q4_gemm_mx_workspace(int(M), int(N), int(K)))
 
 
 def q4_gemm_experts_workspace(T: int, E: int, N: int, K: int) -> int:
-    """Bytes of workspace that q4_gemm_experts needs (-1 for sizes it refuses)."""
+    """Bytes of workspace that q4_gemm_experts needs (0: none, -1: it refuses the sizes)."""
     return int(load().q4_gemm_experts_workspace(int(T), int(E), int(N), int(K)))
 
 
@@ -518,15 +530,16 @@ def q4_gemm_mx(codes: torch.Tensor, scales: torch.Tensor, x: torch.Tensor, y: to
         raise ValueError("codes is a stack of matrices: use q4_gemm_experts")
     _operand(x, "x", _BF16, x.shape, codes)
     lib = load()
-    with _On(codes, stream) as on:
+    handle, context = _on(codes, stream)
+    with context:
         if y is None:
             _type(dtype, _OUT, "dtype")
-            y = on.empty((M, N), dtype)
+            y = torch.empty((M, N), dtype=dtype, device=codes.device)
         else:
             _operand(y, "y", _OUT, (M, N), codes)
-        workspace = _scratch(on, workspace, lib.q4_gemm_mx_workspace(M, N, K), codes, "q4_gemm_mx")
+        at, size, _hold = _scratch(workspace, lib.q4_gemm_mx_workspace(M, N, K), codes, "q4_gemm_mx")
         st = lib.q4_gemm_mx(codes.data_ptr(), scales.data_ptr(), x.data_ptr(), y.data_ptr(), _TYPE[y.dtype],
-                            M, N, K, workspace.data_ptr(), workspace.numel(), on.stream)
+                            M, N, K, at, size, handle)
     _check(st, "q4_gemm_mx")
     return y
 
@@ -553,17 +566,17 @@ def q4_gemm_experts(codes: torch.Tensor, scales: torch.Tensor, x: torch.Tensor, 
         _operand(rows, "rows", _I32, rows.shape, codes)
         T = rows.shape[0]
     lib = load()
-    with _On(codes, stream) as on:
+    handle, context = _on(codes, stream)
+    with context:
         if y is None:
             _type(dtype, _OUT, "dtype")
-            y = on.empty((T, N), dtype)
+            y = torch.empty((T, N), dtype=dtype, device=codes.device)
         else:
             _operand(y, "y", _OUT, (T, N), codes)
-        workspace = _scratch(on, workspace, lib.q4_gemm_experts_workspace(T, E, N, K), codes, "q4_gemm_experts")
+        at, size, _hold = _scratch(workspace, lib.q4_gemm_experts_workspace(T, E, N, K), codes, "q4_gemm_experts")
         st = lib.q4_gemm_experts(codes.data_ptr(), scales.data_ptr(), x.data_ptr(),
                                  None if rows is None else rows.data_ptr(), offsets.data_ptr(),
-                                 y.data_ptr(), _TYPE[y.dtype], Mx, T, E, N, K, workspace.data_ptr(),
-                                 workspace.numel(), on.stream)
+                                 y.data_ptr(), _TYPE[y.dtype], Mx, T, E, N, K, at, size, handle)
     _check(st, "q4_gemm_experts")
     return y
 
@@ -579,21 +592,22 @@ def q4_sort_experts(ids: torch.Tensor, E: int, offsets: torch.Tensor = None, row
     _operand(ids, "ids", _IDS, ids.shape, ids)
     if E < 1 or top < 1:
         raise ValueError(f"E = {E} and top = {top} must be at least 1")
-    with _On(ids, stream) as on:
+    handle, context = _on(ids, stream)
+    with context:
         if offsets is None:
-            offsets = on.empty(E + 1, torch.int32)
+            offsets = torch.empty(E + 1, dtype=torch.int32, device=ids.device)
         else:
             _operand(offsets, "offsets", _I32, (E + 1,), ids)
         if rows is None:
-            rows = on.empty(M * top, torch.int32)
+            rows = torch.empty(M * top, dtype=torch.int32, device=ids.device)
         else:
             _operand(rows, "rows", _I32, (M * top,), ids)
         if places is None:
-            places = on.empty((M, top), torch.int32)
+            places = torch.empty((M, top), dtype=torch.int32, device=ids.device)
         else:
             _operand(places, "places", _I32, (M, top), ids)
         st = load().q4_sort_experts(ids.data_ptr(), int(ids.dtype == torch.int64), offsets.data_ptr(),
-                                    rows.data_ptr(), places.data_ptr(), M, top, E, on.stream)
+                                    rows.data_ptr(), places.data_ptr(), M, top, E, handle)
     _check(st, "q4_sort_experts")
     return offsets, rows, places
 
@@ -613,13 +627,14 @@ def q4_dispatch(x: torch.Tensor, places: torch.Tensor, xs: torch.Tensor = None, 
     """xs [M * top, K]: the rows of x [M, K] at their choices' places, zeros at
     dropped ones.  The gradient is q4_combine(dxs, places)."""
     M, top, K = _row_sizes(x, "x", places, True)
-    with _On(x, stream) as on:
+    handle, context = _on(x, stream)
+    with context:
         if xs is None:
-            xs = on.empty((M * top, K), x.dtype)
+            xs = torch.empty((M * top, K), dtype=x.dtype, device=x.device)
         else:
             _operand(xs, "xs", (x.dtype,), (M * top, K), x)
         st = load().q4_dispatch(x.data_ptr(), places.data_ptr(), xs.data_ptr(), _TYPE[x.dtype], M, top, K,
-                                on.stream)
+                                handle)
     _check(st, "q4_dispatch")
     return xs
 
@@ -632,13 +647,14 @@ def q4_combine(ys: torch.Tensor, places: torch.Tensor, weights: torch.Tensor = N
     M, top, K = _row_sizes(ys, "ys", places, False)
     if weights is not None:
         _operand(weights, "weights", _F32, (M, top), ys)
-    with _On(ys, stream) as on:
+    handle, context = _on(ys, stream)
+    with context:
         if out is None:
-            out = on.empty((M, K), ys.dtype)
+            out = torch.empty((M, K), dtype=ys.dtype, device=ys.device)
         else:
             _operand(out, "out", (ys.dtype,), (M, K), ys)
         st = load().q4_combine(ys.data_ptr(), places.data_ptr(), None if weights is None else weights.data_ptr(),
-                               out.data_ptr(), _TYPE[ys.dtype], M, top, K, on.stream)
+                               out.data_ptr(), _TYPE[ys.dtype], M, top, K, handle)
     _check(st, "q4_combine")
     return out
 
@@ -650,17 +666,18 @@ def q4_combine_grad(dout: torch.Tensor, ys: torch.Tensor, places: torch.Tensor, 
     M, top, K = _row_sizes(ys, "ys", places, False)
     _operand(dout, "dout", (ys.dtype,), (M, K), ys)
     _operand(weights, "weights", _F32, (M, top), ys)
-    with _On(ys, stream) as on:
+    handle, context = _on(ys, stream)
+    with context:
         if dys is None:
-            dys = on.empty((M * top, K), ys.dtype)
+            dys = torch.empty((M * top, K), dtype=ys.dtype, device=ys.device)
         else:
             _operand(dys, "dys", (ys.dtype,), (M * top, K), ys)
         if dweights is None:
-            dweights = on.empty((M, top), torch.float32)
+            dweights = torch.empty((M, top), dtype=torch.float32, device=ys.device)
         else:
             _operand(dweights, "dweights", _F32, (M, top), ys)
         st = load().q4_combine_grad(dout.data_ptr(), ys.data_ptr(), places.data_ptr(), weights.data_ptr(),
-                                    dys.data_ptr(), dweights.data_ptr(), _TYPE[ys.dtype], M, top, K, on.stream)
+                                    dys.data_ptr(), dweights.data_ptr(), _TYPE[ys.dtype], M, top, K, handle)
     _check(st, "q4_combine_grad")
     return dys, dweights
 

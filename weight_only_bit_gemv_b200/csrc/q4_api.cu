@@ -10,7 +10,7 @@ namespace q4 {
 namespace {
 
 constexpr int kMaxDevices = 64;
-constexpr int kMaxSlots = 112;
+constexpr int kMaxSlots = 128;
 
 struct Cache {
     std::mutex mu;
@@ -422,13 +422,14 @@ q4_status q4_bounds_flags(uint32_t* flags) {
     if (!flags) return Q4_ERR_NULL;
     *flags = 0;
     cudaError_t e = cudaDeviceSynchronize();
-    cudaError_t (*const take[9])(unsigned int*) = {
+    cudaError_t (*const take[10])(unsigned int*) = {
         take_bounds_gemv_m1, take_bounds_gemm_small, take_bounds_gemm_tc, take_bounds_gemv, take_bounds_pack,
-        take_bounds_gemv2,   take_bounds_mx_pack,    take_bounds_mx_gemm, take_bounds_experts};
-    for (int i = 0; i < 9 && e == cudaSuccess; ++i) {
+        take_bounds_gemv2,   take_bounds_mx_pack,    take_bounds_mx_gemm, take_bounds_experts,
+        take_bounds_mx_decode};
+    for (int i = 0; i < 10 && e == cudaSuccess; ++i) {
         unsigned int v = 0;
         e = take[i](&v);
-        if (v) *flags |= 1u << i;
+        if (v) *flags |= 1u << (i == 9 ? 7 : i);  // both kernels of the microscaled products
     }
     return e == cudaSuccess ? Q4_OK : cuda_fail(e);
 }
@@ -506,14 +507,15 @@ q4_status q4_gemv2(const uint8_t* codes, const uint16_t* scales, const uint16_t*
 q4_status q4_timeout_flags(uint32_t* flags) {
     if (!flags) return Q4_ERR_NULL;
     *flags = 0;
-    unsigned int a = 0, b = 0, c = 0, d = 0, m = 0;
+    unsigned int a = 0, b = 0, c = 0, d = 0, m = 0, m8 = 0;
     cudaError_t e = take_gemv_m1_error(&a);
     if (e == cudaSuccess) e = take_gemm_tc_error(&b);
     if (e == cudaSuccess) e = take_gemm_small_error(&c);
     if (e == cudaSuccess) e = take_gemv2_error(&d);
     if (e == cudaSuccess) e = take_gemm_mx_error(&m);
+    if (e == cudaSuccess) e = take_decode_mx_error(&m8);
     if (e != cudaSuccess) return cuda_fail(e);
-    *flags = (a & 0x0FF0u) | (d & 0x000Eu) | ((c & 0x0F00u) << 4) | ((b & 0xFFFFu) << 16) | (m ? 1u : 0u);
+    *flags = (a & 0x0FF0u) | (d & 0x000Eu) | ((c & 0x0F00u) << 4) | ((b & 0xFFFFu) << 16) | (m || m8 ? 1u : 0u);
     return Q4_OK;
 }
 
@@ -581,7 +583,7 @@ static q4_status run_gemm_mx(const uint8_t* codes, const uint8_t* scales, const 
     if (grouped && !rows && Mx != T) return Q4_ERR_SHAPE;
     const int64_t need = gemm_mx_workspace(T, E, N, K);
     if (need < 0) return Q4_ERR_SHAPE;
-    if (!codes || !scales || !x || !y || !workspace || (grouped && !offsets)) return Q4_ERR_NULL;
+    if (!codes || !scales || !x || !y || (need > 0 && !workspace) || (grouped && !offsets)) return Q4_ERR_NULL;
     if ((reinterpret_cast<uintptr_t>(codes) & 31u) || !aligned16(scales) || !aligned16(x) || !aligned16(rows) ||
         !aligned16(offsets) || !aligned16(y) || !aligned16(workspace))
         return Q4_ERR_ALIGN;

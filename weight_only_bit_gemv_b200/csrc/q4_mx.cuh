@@ -60,12 +60,16 @@ cudaError_t launch_pack_mx(const void* w, int type, uint8_t* codes, uint8_t* sca
 cudaError_t launch_dequant_mx(const uint8_t* codes, const uint8_t* scales, void* w, int type, int64_t E,
                               int64_t N, int64_t K, cudaStream_t s);
 // offsets == nullptr: one matrix (E = 1), T rows of x in order.
-// -1: more k blocks of output tiles than 2^31 - 1.
+// -1: more k blocks of output tiles than 2^31 - 1.  0: none is needed.
 int64_t gemm_mx_workspace(int64_t T, int64_t E, int64_t N, int64_t K);
 cudaError_t launch_gemm_mx(const uint8_t* codes, const uint8_t* scales, const uint16_t* x,
                            const int32_t* rows, const int32_t* offsets, void* y, int y_type, int64_t Mx,
                            int64_t T, int64_t E, int64_t N, int64_t K, void* workspace, cudaStream_t s,
                            const DeviceInfo& dev);
+// At most 8 tokens a tile, `split` CTAs of a cluster to a tile, no workspace.
+cudaError_t launch_decode_mx(const uint8_t* codes, const uint8_t* scales, const uint16_t* x, const int32_t* rows,
+                             const int32_t* offsets, void* y, int y_type, int64_t Mx, int64_t T, int64_t E, int64_t N,
+                             int64_t K, int split, int groups, cudaStream_t s, const DeviceInfo& dev);
 cudaError_t launch_sort_experts(const void* ids, int wide, int32_t* offsets, int32_t* rows, int32_t* places,
                                 int64_t M, int64_t top, int64_t E, cudaStream_t s, const DeviceInfo& dev);
 cudaError_t launch_dispatch(const void* x, const int32_t* places, void* xs, int type, int64_t M, int64_t top,
@@ -77,8 +81,10 @@ cudaError_t launch_combine_grad(const void* dout, const void* ys, const int32_t*
                                 cudaStream_t s);
 
 cudaError_t take_gemm_mx_error(unsigned int* out);
+cudaError_t take_decode_mx_error(unsigned int* out);
 cudaError_t take_bounds_mx_pack(unsigned int* out);
 cudaError_t take_bounds_mx_gemm(unsigned int* out);
+cudaError_t take_bounds_mx_decode(unsigned int* out);
 cudaError_t take_bounds_experts(unsigned int* out);
 
 }  // namespace q4

@@ -39,8 +39,7 @@
 // drains its copies, frees its tensor memory and exits.
 #include <algorithm>
 
-#include "q4_mx.cuh"
-#include "q4_sm100.cuh"
+#include "q4_mx_tc.cuh"
 
 namespace q4 {
 
@@ -52,8 +51,6 @@ constexpr int kThreads = 192;     // producer, MMA, four epilogue warps
 constexpr int kFlush32 = 8;       // k blocks per accumulation in tensor memory, binary32 y
 constexpr int kFlush16 = 64;      // ... bfloat16 y
 constexpr int kMinBlocks = 4;     // least k blocks a CTA is started for
-constexpr uint32_t kTmemCols = 512;
-constexpr int kMaxExperts = Q4_MAX_EXPERTS;
 constexpr int kPairTokens = 120;  // most tokens of a pair's tile: two accumulators of 240 columns
 
 struct MxGemm {
@@ -113,268 +110,8 @@ Workspace workspace_layout(int64_t T, int64_t E, int64_t N, int64_t K, const Pla
 }
 
 // ---------------------------------------------------------------------------
-// device helpers
+// x to its two parts, in the order of the token tiles
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-
-// tcgen05 instructions of one CTA (kCtas = 1) or of a pair (2): one thread of
-// the pair's first CTA then acts for both, each CTA's own shared and tensor
-// memory at the same addresses.
-#define Q4_TC(one, two, ...)                  \
-    do {                                      \
-        if constexpr (kCtas == 1)             \
-            asm volatile(one __VA_ARGS__);    \
-        else                                  \
-            asm volatile(two __VA_ARGS__);    \
-    } while (0)
-
-// 512 exponent bytes from shared memory to four columns of tensor memory,
-// repeated in the four lane quarters.
-template <int kCtas>
-__device__ __forceinline__ void tc_copy_scales(uint32_t taddr, uint64_t desc) {
-    Q4_TC("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;", "tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;",
-          ::"r"(taddr), "l"(desc) : "memory");
-}
-
-// D[tmem] (+)= (A * sfa) x (B * sfb)^T, both operands in shared memory.
-template <int kCtas>
-__device__ __forceinline__ void tc_mma_mx(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
-                                          uint32_t sfb, uint32_t accumulate) {
-    Q4_TC("{\n\t.reg .pred p;\n\t"
-          "setp.ne.b32 p, %6, 0;\n\t"
-          "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}",
-          "{\n\t.reg .pred p;\n\t"
-          "setp.ne.b32 p, %6, 0;\n\t"
-          "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}",
-          ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate) : "memory");
-}
-
-// One arrival on `bar`, in every CTA of the group, when all prior MMAs and
-// copies of this thread are complete.
-template <int kCtas>
-__device__ __forceinline__ void tc_commit_all(uint32_t bar) {
-    if constexpr (kCtas == 1)
-        tc_commit(bar);
-    else
-        asm volatile(
-            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-            "h"(static_cast<uint16_t>(3))
-            : "memory");
-}
-template <int kCtas>
-__device__ __forceinline__ void tc_commit_own(uint32_t bar) {
-    Q4_TC("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];",
-          "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];", ::"r"(bar) : "memory");
-}
-template <int kCtas>
-__device__ __forceinline__ void tmem_alloc_all(uint32_t dst) {
-    Q4_TC("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;",
-          "tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;", ::"r"(dst), "r"(kTmemCols) : "memory");
-    Q4_TC("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;",
-          "tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;", ::: "memory");
-}
-template <int kCtas>
-__device__ __forceinline__ void tmem_free_all(uint32_t taddr) {
-    Q4_TC("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;", "tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;",
-          ::"r"(taddr), "r"(kTmemCols) : "memory");
-}
-#undef Q4_TC
-
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm("mov.u32 %0, %cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// The address in the pair's first CTA of what is at `addr` in this one.
-__device__ __forceinline__ uint32_t in_first_cta(uint32_t addr) {
-    uint32_t a;
-    asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(addr));
-    return a;
-}
-__device__ __forceinline__ void arrive_cluster(uint32_t bar) {
-    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-// TMA loads into this CTA that complete on a barrier of either CTA of the pair.
-__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap* map, int c0, int c1, uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
-        "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
-        : "memory");
-}
-__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2,
-                                                 uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
-        "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
-        : "memory");
-}
-
-// Descriptor of 32 rows of 16 bytes in a row (no swizzle), for tc_copy_scales.
-__device__ __forceinline__ uint64_t scale_desc(uint32_t saddr) {
-    return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (1ull << 16) | (static_cast<uint64_t>(128 >> 4) << 32) |
-           (1ull << 46);
-}
-
-// Instruction descriptor: A e2m1, B e4m3, power-of-two scales; the scale byte
-// q of each 32-bit column is taken on both sides.
-__host__ __device__ constexpr uint32_t mx_idesc(int M, int N, int q) {
-    return (static_cast<uint32_t>(q) << 4) | (5u << 7) | (0u << 10) | (static_cast<uint32_t>(N >> 3) << 17) |
-           (1u << 23) | (static_cast<uint32_t>(M >> 4) << 24) | (static_cast<uint32_t>(q) << 29);
-}
-
-// One lane of a converged warp.  The producer and MMA warps run their loops
-// with all lanes, so that addresses and descriptors stay in uniform registers,
-// and only issue with one (with `if (lane == 0)` around the loop each MMA took
-// 70 cycles to issue and a stage's bookkeeping 450).
-__device__ __forceinline__ bool elect_one() {
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "elect.sync _|p, 0xFFFFFFFF;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(r));
-    return r != 0u;
-}
-
-// mbar_wait that also gives up once another role has.
-__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag) {
-    if (mbar_try_wait(bar, parity)) return true;
-    const unsigned long long t0 = globaltimer_ns();
-    while (true) {
-        for (int i = 0; i < 64; ++i)
-            if (mbar_try_wait(bar, parity)) return true;
-        if (*abort_flag || globaltimer_ns() - t0 > kWaitLimitNs) return false;
-    }
-}
-
-// A ring's slot and the parity of its use, without divisions.
-template <int kSlots>
-struct Ring {
-    int slot = 0;
-    uint32_t parity = 0;
-    __device__ void next() {
-        if (++slot == kSlots) {
-            slot = 0;
-            parity ^= 1u;
-        }
-    }
-};
-
-// 3-D TMA load of one box into shared memory, completing on `bar`.
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2,
-                                            uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes "
-        "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
-        : "memory");
-}
-
-// Barrier of the four epilogue warps; true if `ok` was true in all of them.
-// They leave their loop only on its result, so none waits for one that left.
-__device__ __forceinline__ bool epilogue_sync(bool ok) {
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.u32 p, %1, 0;\n\t"
-        "barrier.cta.red.and.pred q, 1, 128, p;\n\t"
-        "selp.u32 %0, 1, 0, q;\n\t}"
-        : "=r"(r)
-        : "r"(ok ? 1u : 0u)
-        : "memory");
-    return r != 0u;
-}
-
-// Row ranges of the experts and the token tiles before each, in shared
-// memory: offset[e], tile[e] for e in [0, E].  Offsets are taken as
-// non-decreasing values in [0, T]; anything else is clamped to that.
-struct Table {
-    int offset[kMaxExperts + 1];
-    int tile[kMaxExperts + 1];
-};
-
-__device__ void fill_table(Table& t, const int32_t* __restrict__ offsets, int E, int T, int tokens) {
-    if (!offsets) {
-        if (threadIdx.x == 0) {
-            t.offset[0] = 0;
-            t.offset[1] = T;
-            t.tile[0] = 0;
-            t.tile[1] = (T + tokens - 1) / tokens;
-        }
-    } else if (threadIdx.x < 32) {
-        const int lane = threadIdx.x;
-        int high = 0, tiles = 0;  // over the experts before this round
-        for (int e0 = 0; e0 < E; e0 += 32) {
-            const int e = e0 + lane;
-            int first = e < E && Q4_IN_BOUNDS(e, 2, E + 1) ? min(max(__ldg(offsets + e), 0), T) : 0;
-            int last = e < E ? min(max(__ldg(offsets + e + 1), 0), T) : 0;
-            // running maxima: first is at least every earlier end
-            int top = max(first, last);
-#pragma unroll
-            for (int d = 1; d < 32; d *= 2) {
-                const int o = __shfl_up_sync(0xFFFFFFFFu, top, d);
-                if (lane >= d) top = max(top, o);
-            }
-            const int up = __shfl_up_sync(0xFFFFFFFFu, top, 1);
-            const int before = max(high, lane ? up : 0);
-            first = max(first, before);
-            last = max(last, first);
-            const int mine = e < E ? (last - first + tokens - 1) / tokens : 0;
-            int sum = mine;
-#pragma unroll
-            for (int d = 1; d < 32; d *= 2) {
-                const int o = __shfl_up_sync(0xFFFFFFFFu, sum, d);
-                if (lane >= d) sum += o;
-            }
-            if (e < E) {
-                t.offset[e] = first;
-                t.tile[e] = tiles + sum - mine;
-                if (e == E - 1) {
-                    t.offset[E] = last;
-                    t.tile[E] = tiles + sum;
-                }
-            }
-            high = max(high, __shfl_sync(0xFFFFFFFFu, top, 31));
-            tiles += __shfl_sync(0xFFFFFFFFu, sum, 31);
-        }
-    }
-    __syncthreads();
-}
-
-// The last e with first[e] <= v (first[0] <= v < first[E]).
-__device__ __forceinline__ int find_expert(const int* first, int E, int v) {
-    int lo = 0, hi = E;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) / 2;
-        if (first[mid] <= v)
-            lo = mid;
-        else
-            hi = mid;
-    }
-    return lo;
-}
-
-// ---------------------------------------------------------------------------
-// x to its two e4m3 parts, in the order of the token tiles
-// ---------------------------------------------------------------------------
-// Eight binary32 values to e4m3 and back.
-__device__ __forceinline__ uint32_t to_e4m3x2(float a, float b) {
-    uint16_t r;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %2, %1;" : "=h"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ float2 from_e4m3x2(uint32_t v) {
-    uint32_t h;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(v)));
-    return __half22float2(*reinterpret_cast<const __half2*>(&h));
-}
-
 struct Convert {
     const uint16_t* x;
     const int32_t* rows;  // x row of each of the T rows; nullptr: the row itself
@@ -420,68 +157,19 @@ __global__ void __launch_bounds__(256) convert_kernel(const Convert p) {
         const int64_t k = piece * 256 + 8 * lane;
         const int kb = 2 * piece + lane / 16;
         float v[8];
-        if (kVector) {
-            uint4 q = make_uint4(0, 0, 0, 0);
-            if (have && k < p.K && Q4_IN_BOUNDS(src * p.K + k, 8, p.Mx * p.K))
-                q = __ldg(reinterpret_cast<const uint4*>(p.x + src * p.K + k));
-            const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                v[2 * j] = __uint_as_float(w[j] << 16);
-                v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                v[j] = have && k + j < p.K && Q4_IN_BOUNDS(src * p.K + k + j, 1, p.Mx * p.K)
-                           ? bf16_bits_to_float(p.x[src * p.K + k + j]) : 0.0f;
-        }
-        uint32_t top = 0;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(v[j]) & 0x7FFFFFFFu);
-        top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-        top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-        // hi's exponent byte: the largest value's field - 7, so that the
-        // largest x / s is in [128, 256); at least 5, which leaves lo's >= 0
-        const uint32_t field = top >> 23;
-        const uint32_t byte = field > 12u ? field - 7u : 5u;
-        const float inverse = __uint_as_float((254u - byte) << 23);
-        uint2 hi, lo;
-        uint32_t* hp = &hi.x;
-        uint32_t* lp = &lo.x;
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            uint32_t h = 0, l = 0;
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const float a = v[4 * j + 2 * i] * inverse, b = v[4 * j + 2 * i + 1] * inverse;
-                const uint32_t c = to_e4m3x2(a, b);
-                const float2 back = from_e4m3x2(c);
-                h |= c << (16 * i);
-                l |= to_e4m3x2((a - back.x) * 32.0f, (b - back.y) * 32.0f) << (16 * i);
-            }
-            hp[j] = h;
-            lp[j] = l;
-        }
+        unpack_x8(load_x8<kVector>(p.x, have, src * p.K + k, k, p.K, p.Mx * p.K), v);
+        const XParts parts = split_x(v);
         if (kb < p.Kb) {
             const int64_t Kp = static_cast<int64_t>(p.Kb) * kMxBlock;
             [[maybe_unused]] const int64_t extent = p.tile_limit * 2 * p.tokens * Kp;
             const int64_t at = (tile * 2 * p.tokens + m) * Kp + k;
             if (Q4_IN_BOUNDS(at, 8, extent) && Q4_IN_BOUNDS(at + p.tokens * Kp, 8, extent)) {
-                *reinterpret_cast<uint2*>(p.xq + at) = hi;
-                *reinterpret_cast<uint2*>(p.xq + at + p.tokens * Kp) = lo;
+                *reinterpret_cast<uint2*>(p.xq + at) = parts.hi;
+                *reinterpret_cast<uint2*>(p.xq + at + p.tokens * Kp) = parts.lo;
             }
         }
-        // the four groups of a k block: one 32-bit store per part.  A group
-        // with an infinity or NaN gets the exponent byte of NaN.
-        const uint32_t mine = field == 255u ? 255u : byte;
-        uint32_t four = 0, four_lo = 0;
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-            const uint32_t b = __shfl_sync(0xFFFFFFFFu, mine, (lane & 16) + 4 * g);
-            four |= b << (8 * g);
-            four_lo |= (b == 255u ? 255u : b - 5u) << (8 * g);
-        }
+        uint32_t four, four_lo;
+        gather_bytes(parts.byte, lane, four, four_lo);
         if ((lane & 15) == 0 && kb < p.Kb) {
             [[maybe_unused]] const int64_t extent = p.tile_limit * p.x_blocks * p.Kb * kMxScaleBytes;
             const int r = p.tokens + m;
@@ -1041,9 +729,41 @@ cudaError_t launch_as(const Plan& plan, const uint8_t* codes, const uint8_t* sca
 
 }  // namespace
 
+// Whether a product with tiles of 8 tokens runs on q4_mx_decode.cu, and how:
+// the CTAs that share a tile's K (0: not at all), and how many such groups.
+// Counted in stages of 256 k, 0.31 us each on one SM (0.42 us with more than 4
+// tokens, whose x takes longer to prepare than the codes to come): a turn of a
+// group costs half a stage beside its own, sharing a tile 5 stages once, and
+// the kernel above 21 for its second launch and its sums' way through memory.
+// Measured on B200 (us, 1 token; 1, 2, 4 CTAs a tile; the kernel above):
+//   4096 x 4096   8.0  6.8  5.8;  9.5     28672 x 4096  14.9 16.1 14.4; 17.7
+//   4096 x 14336 21.0 13.5 10.0; 12.1     28672 x 8192  26.0 27.6 24.4; 26.6
+//   128256 x 4096 44.7 46.0 47.3; 49.6    28672 x 8192, 8 tokens 32.2 33.6 31.6; 27.0
+struct DecodePlan {
+    int split, groups;
+};
+static DecodePlan decode_plan(int64_t tiles, int64_t Kb, int64_t share) {
+    const int64_t Ku = (Kb + 1) / 2;
+    const double stage = share > 4 ? 1.35 : 1.0;
+    DecodePlan best{0, 0};
+    double least = static_cast<double>(tiles) * Ku / 148 + 21.0;
+    for (int split = 1; split <= 4; split *= 2) {
+        const int most = split == 1 ? 148 : split == 2 ? 74 : 33;  // groups that run at once
+        const int64_t turns = (tiles + most - 1) / most;
+        const double cost = (turns * ((Ku + split - 1) / split + 0.5) + (split == 1 ? 0.0 : 5.0)) * stage;
+        if (cost < least) {
+            least = cost;
+            best = {split, static_cast<int>(std::min<int64_t>(tiles, most))};
+        }
+    }
+    return best;
+}
+
 int64_t gemm_mx_workspace(int64_t T, int64_t E, int64_t N, int64_t K) {
-    const Workspace l = workspace_layout(T, E, N, K, plan_for(T, E));
+    const Plan plan = plan_for(T, E);
+    const Workspace l = workspace_layout(T, E, N, K, plan);
     if (l.tiles > INT32_MAX / (mx_blocks(N) * mx_blocks(K))) return -1;
+    if (plan.tokens == 8 && decode_plan(l.tiles * mx_blocks(N), mx_blocks(K), (T + E - 1) / E).split > 0) return 0;
     return static_cast<int64_t>(l.bytes);
 }
 
@@ -1052,6 +772,11 @@ cudaError_t launch_gemm_mx(const uint8_t* codes, const uint8_t* scales, const ui
                            int64_t K, void* workspace, cudaStream_t s, const DeviceInfo& dev) {
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     const Plan plan = plan_for(T, E);
+    if (plan.tokens == 8) {
+        const DecodePlan d = decode_plan(workspace_layout(T, E, N, K, plan).tiles * mx_blocks(N), mx_blocks(K), (T + E - 1) / E);
+        if (d.split > 0)
+            return launch_decode_mx(codes, scales, x, rows, offsets, y, y_type, Mx, T, E, N, K, d.split, d.groups, s, dev);
+    }
     const auto launch = plan.pair           ? launch_as<kPairTokens, 2>
                         : plan.tokens == 8  ? launch_as<8, 1>
                         : plan.tokens == 16 ? launch_as<16, 1>
