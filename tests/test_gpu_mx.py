@@ -3,6 +3,10 @@ dequant bit for bit, products within a bound counted from the arithmetic
 (mx_reference.tolerance) and exactly where every sum is exact."""
 from __future__ import annotations
 
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -284,6 +288,39 @@ def test_gemm_in_graphs():
         torch.cuda.synchronize()
         for g, x, y, w, s in made:
             _close(y, w, x)
+
+
+FIRST_CALL = """
+import sys
+sys.path[:0] = [{root!r}, {tests!r}]
+import numpy as np, torch
+import weight_only_bit_gemv_b200 as q4
+from test_gpu_mx import _close, _packed, _x
+torch.cuda.set_device(0)
+rng = np.random.default_rng(1)
+codes, scales, w = _packed(rng, 300, 700, 3)
+x = [_x(rng, M, 700) for M in (2, 12, 30, 60, 150)]
+ids = torch.from_numpy(rng.integers(0, 3, (2, 2))).cuda()
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    ys = [q4.q4_gemm_mx(codes[0], scales[0], v, N=300) for v in x]
+    offsets, rows, places = q4.q4_sort_experts(ids, 3)
+    out = q4.q4_combine(q4.q4_gemm_experts(codes, scales, x[0], offsets, rows, N=300), places)
+g.replay()
+torch.cuda.synchronize()
+for v, y in zip(x, ys):
+    _close(y, w[0], v)
+print("captured")
+"""
+
+
+def test_first_calls_may_be_captured():
+    """A process whose first calls of every kernel are made under capture."""
+    tests = os.path.dirname(os.path.abspath(__file__))
+    code = FIRST_CALL.format(root=os.path.dirname(tests), tests=tests)
+    res = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert res.returncode == 0 and "captured" in res.stdout, res.stdout + res.stderr
 
 
 def test_gemm_empty():

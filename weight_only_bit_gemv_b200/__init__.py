@@ -27,7 +27,6 @@ allocate belongs to the stream that they run on.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 import re
@@ -380,17 +379,9 @@ class _Foreign:
             g.__exit__(*exc)
 
 
-_HERE_ALREADY = contextlib.nullcontext()
-
-
-def _on(t: torch.Tensor, stream):
-    """(stream handle, context) of a call on ``t``'s device and ``stream``, the
-    device's current one if None."""
-    index = t.get_device()
-    if stream is not None:
-        return int(getattr(stream, "cuda_stream", stream)), _Foreign(index, stream)
-    return (torch._C._cuda_getCurrentRawStream(index),
-            _HERE_ALREADY if index == torch._C._cuda_getDevice() else _Foreign(index, None))
+def _elsewhere(t: torch.Tensor, stream) -> bool:
+    """Whether a call on ``t``'s device and ``stream`` has to enter _Foreign."""
+    return stream is not None or t.get_device() != torch._C._cuda_getDevice()
 
 
 def _operand(t, name: str, dtypes, shape, on: torch.Tensor) -> None:
@@ -435,16 +426,20 @@ def _type(dtype, allowed, name: str) -> int:
 def _mx_sizes(codes, scales, N, K):
     """(E or None, N, K) of a packed matrix or stack, checked against its blocks."""
     _dims(codes, "codes", (4, 5), "[Nb, Kb, 128, 64] or [E, Nb, Kb, 128, 64]")
-    lead, (nb, kb) = codes.shape[:-4], codes.shape[-4:-2]
-    if codes.shape[-2:] != (MX_BLOCK, MX_BLOCK // 2):
+    shape = codes.shape
+    nb, kb = shape[-4], shape[-3]
+    if shape[-2] != MX_BLOCK or shape[-1] != MX_BLOCK // 2:
         raise ValueError("codes must be [..., Nb, Kb, 128, 64]")
     N = nb * MX_BLOCK if N is None else int(N)
     K = kb * MX_BLOCK if K is None else int(K)
     if -(-N // MX_BLOCK) != nb or -(-K // MX_BLOCK) != kb or N < 0:
         raise ValueError(f"N = {N}, K = {K} do not have {nb} x {kb} blocks of {MX_BLOCK}")
-    _operand(codes, "codes", _BYTES, codes.shape, codes)
-    _operand(scales, "scales", _BYTES, (*lead, nb, kb, 512), codes)
-    return (lead[0] if lead else None), N, K
+    _operand(codes, "codes", _BYTES, shape, codes)
+    if len(shape) == 4:
+        _operand(scales, "scales", _BYTES, (nb, kb, 512), codes)
+        return None, N, K
+    _operand(scales, "scales", _BYTES, (shape[0], nb, kb, 512), codes)
+    return shape[0], N, K
 
 
 def q4_pack_mx(w: torch.Tensor, codes: torch.Tensor = None, scales: torch.Tensor = None, stream=None):
@@ -455,18 +450,20 @@ def q4_pack_mx(w: torch.Tensor, codes: torch.Tensor = None, scales: torch.Tensor
     lead = tuple(w.shape[:-2])
     nb, kb = -(-N // MX_BLOCK), -(-K // MX_BLOCK)
     _operand(w, "w", _FLOATS, w.shape, w)
-    handle, context = _on(w, stream)
-    with context:
-        if codes is None:
-            codes = torch.empty((*lead, nb, kb, MX_BLOCK, MX_BLOCK // 2), dtype=torch.uint8, device=w.device)
-        else:
-            _operand(codes, "codes", _BYTES, (*lead, nb, kb, MX_BLOCK, MX_BLOCK // 2), w)
-        if scales is None:
-            scales = torch.empty((*lead, nb, kb, 512), dtype=torch.uint8, device=w.device)
-        else:
-            _operand(scales, "scales", _BYTES, (*lead, nb, kb, 512), w)
-        st = load().q4_pack_mx(w.data_ptr(), _TYPE[w.dtype], codes.data_ptr(), scales.data_ptr(),
-                               lead[0] if lead else 1, N, K, handle)
+    if _elsewhere(w, stream):
+        with _Foreign(w.get_device(), stream):
+            return q4_pack_mx(w, codes, scales)
+    handle = torch._C._cuda_getCurrentRawStream(w.get_device())
+    if codes is None:
+        codes = torch.empty(*lead, nb, kb, MX_BLOCK, MX_BLOCK // 2, dtype=torch.uint8, device=w.device)
+    else:
+        _operand(codes, "codes", _BYTES, (*lead, nb, kb, MX_BLOCK, MX_BLOCK // 2), w)
+    if scales is None:
+        scales = torch.empty(*lead, nb, kb, 512, dtype=torch.uint8, device=w.device)
+    else:
+        _operand(scales, "scales", _BYTES, (*lead, nb, kb, 512), w)
+    st = load().q4_pack_mx(w.data_ptr(), _TYPE[w.dtype], codes.data_ptr(), scales.data_ptr(),
+                           lead[0] if lead else 1, N, K, handle)
     _check(st, "q4_pack_mx")
     return codes, scales
 
@@ -477,15 +474,17 @@ def q4_dequant_mx(codes: torch.Tensor, scales: torch.Tensor, w_out: torch.Tensor
     ``dtype``.  N and K default to whole blocks."""
     E, N, K = _mx_sizes(codes, scales, N, K)
     shape = (N, K) if E is None else (E, N, K)
-    handle, context = _on(codes, stream)
-    with context:
-        if w_out is None:
-            _type(dtype, _FLOATS, "dtype")
-            w_out = torch.empty(shape, dtype=dtype, device=codes.device)
-        else:
-            _operand(w_out, "w_out", _FLOATS, shape, codes)
-        st = load().q4_dequant_mx(codes.data_ptr(), scales.data_ptr(), w_out.data_ptr(),
-                                  _TYPE[w_out.dtype], 1 if E is None else E, N, K, handle)
+    if _elsewhere(codes, stream):
+        with _Foreign(codes.get_device(), stream):
+            return q4_dequant_mx(codes, scales, w_out, N, K, dtype)
+    handle = torch._C._cuda_getCurrentRawStream(codes.get_device())
+    if w_out is None:
+        _type(dtype, _FLOATS, "dtype")
+        w_out = torch.empty(*shape, dtype=dtype, device=codes.device)
+    else:
+        _operand(w_out, "w_out", _FLOATS, shape, codes)
+    st = load().q4_dequant_mx(codes.data_ptr(), scales.data_ptr(), w_out.data_ptr(),
+                              _TYPE[w_out.dtype], 1 if E is None else E, N, K, handle)
     _check(st, "q4_dequant_mx")
     return w_out
 
@@ -530,16 +529,18 @@ def q4_gemm_mx(codes: torch.Tensor, scales: torch.Tensor, x: torch.Tensor, y: to
         raise ValueError("codes is a stack of matrices: use q4_gemm_experts")
     _operand(x, "x", _BF16, x.shape, codes)
     lib = load()
-    handle, context = _on(codes, stream)
-    with context:
-        if y is None:
-            _type(dtype, _OUT, "dtype")
-            y = torch.empty((M, N), dtype=dtype, device=codes.device)
-        else:
-            _operand(y, "y", _OUT, (M, N), codes)
-        at, size, _hold = _scratch(workspace, lib.q4_gemm_mx_workspace(M, N, K), codes, "q4_gemm_mx")
-        st = lib.q4_gemm_mx(codes.data_ptr(), scales.data_ptr(), x.data_ptr(), y.data_ptr(), _TYPE[y.dtype],
-                            M, N, K, at, size, handle)
+    if _elsewhere(codes, stream):
+        with _Foreign(codes.get_device(), stream):
+            return q4_gemm_mx(codes, scales, x, y, N, dtype, workspace)
+    handle = torch._C._cuda_getCurrentRawStream(codes.get_device())
+    if y is None:
+        _type(dtype, _OUT, "dtype")
+        y = torch.empty(M, N, dtype=dtype, device=codes.device)
+    else:
+        _operand(y, "y", _OUT, (M, N), codes)
+    at, size, _hold = _scratch(workspace, lib.q4_gemm_mx_workspace(M, N, K), codes, "q4_gemm_mx")
+    st = lib.q4_gemm_mx(codes.data_ptr(), scales.data_ptr(), x.data_ptr(), y.data_ptr(), _TYPE[y.dtype],
+                        M, N, K, at, size, handle)
     _check(st, "q4_gemm_mx")
     return y
 
@@ -566,17 +567,19 @@ def q4_gemm_experts(codes: torch.Tensor, scales: torch.Tensor, x: torch.Tensor, 
         _operand(rows, "rows", _I32, rows.shape, codes)
         T = rows.shape[0]
     lib = load()
-    handle, context = _on(codes, stream)
-    with context:
-        if y is None:
-            _type(dtype, _OUT, "dtype")
-            y = torch.empty((T, N), dtype=dtype, device=codes.device)
-        else:
-            _operand(y, "y", _OUT, (T, N), codes)
-        at, size, _hold = _scratch(workspace, lib.q4_gemm_experts_workspace(T, E, N, K), codes, "q4_gemm_experts")
-        st = lib.q4_gemm_experts(codes.data_ptr(), scales.data_ptr(), x.data_ptr(),
-                                 None if rows is None else rows.data_ptr(), offsets.data_ptr(),
-                                 y.data_ptr(), _TYPE[y.dtype], Mx, T, E, N, K, at, size, handle)
+    if _elsewhere(codes, stream):
+        with _Foreign(codes.get_device(), stream):
+            return q4_gemm_experts(codes, scales, x, offsets, rows, y, N, dtype, workspace)
+    handle = torch._C._cuda_getCurrentRawStream(codes.get_device())
+    if y is None:
+        _type(dtype, _OUT, "dtype")
+        y = torch.empty(T, N, dtype=dtype, device=codes.device)
+    else:
+        _operand(y, "y", _OUT, (T, N), codes)
+    at, size, _hold = _scratch(workspace, lib.q4_gemm_experts_workspace(T, E, N, K), codes, "q4_gemm_experts")
+    st = lib.q4_gemm_experts(codes.data_ptr(), scales.data_ptr(), x.data_ptr(),
+                             None if rows is None else rows.data_ptr(), offsets.data_ptr(),
+                             y.data_ptr(), _TYPE[y.dtype], Mx, T, E, N, K, at, size, handle)
     _check(st, "q4_gemm_experts")
     return y
 
@@ -592,22 +595,24 @@ def q4_sort_experts(ids: torch.Tensor, E: int, offsets: torch.Tensor = None, row
     _operand(ids, "ids", _IDS, ids.shape, ids)
     if E < 1 or top < 1:
         raise ValueError(f"E = {E} and top = {top} must be at least 1")
-    handle, context = _on(ids, stream)
-    with context:
-        if offsets is None:
-            offsets = torch.empty(E + 1, dtype=torch.int32, device=ids.device)
-        else:
-            _operand(offsets, "offsets", _I32, (E + 1,), ids)
-        if rows is None:
-            rows = torch.empty(M * top, dtype=torch.int32, device=ids.device)
-        else:
-            _operand(rows, "rows", _I32, (M * top,), ids)
-        if places is None:
-            places = torch.empty((M, top), dtype=torch.int32, device=ids.device)
-        else:
-            _operand(places, "places", _I32, (M, top), ids)
-        st = load().q4_sort_experts(ids.data_ptr(), int(ids.dtype == torch.int64), offsets.data_ptr(),
-                                    rows.data_ptr(), places.data_ptr(), M, top, E, handle)
+    if _elsewhere(ids, stream):
+        with _Foreign(ids.get_device(), stream):
+            return q4_sort_experts(ids, E, offsets, rows, places)
+    handle = torch._C._cuda_getCurrentRawStream(ids.get_device())
+    if offsets is None:
+        offsets = torch.empty(E + 1, dtype=torch.int32, device=ids.device)
+    else:
+        _operand(offsets, "offsets", _I32, (E + 1,), ids)
+    if rows is None:
+        rows = torch.empty(M * top, dtype=torch.int32, device=ids.device)
+    else:
+        _operand(rows, "rows", _I32, (M * top,), ids)
+    if places is None:
+        places = torch.empty(M, top, dtype=torch.int32, device=ids.device)
+    else:
+        _operand(places, "places", _I32, (M, top), ids)
+    st = load().q4_sort_experts(ids.data_ptr(), int(ids.dtype == torch.int64), offsets.data_ptr(),
+                                rows.data_ptr(), places.data_ptr(), M, top, E, handle)
     _check(st, "q4_sort_experts")
     return offsets, rows, places
 
@@ -627,14 +632,16 @@ def q4_dispatch(x: torch.Tensor, places: torch.Tensor, xs: torch.Tensor = None, 
     """xs [M * top, K]: the rows of x [M, K] at their choices' places, zeros at
     dropped ones.  The gradient is q4_combine(dxs, places)."""
     M, top, K = _row_sizes(x, "x", places, True)
-    handle, context = _on(x, stream)
-    with context:
-        if xs is None:
-            xs = torch.empty((M * top, K), dtype=x.dtype, device=x.device)
-        else:
-            _operand(xs, "xs", (x.dtype,), (M * top, K), x)
-        st = load().q4_dispatch(x.data_ptr(), places.data_ptr(), xs.data_ptr(), _TYPE[x.dtype], M, top, K,
-                                handle)
+    if _elsewhere(x, stream):
+        with _Foreign(x.get_device(), stream):
+            return q4_dispatch(x, places, xs)
+    handle = torch._C._cuda_getCurrentRawStream(x.get_device())
+    if xs is None:
+        xs = torch.empty(M * top, K, dtype=x.dtype, device=x.device)
+    else:
+        _operand(xs, "xs", (x.dtype,), (M * top, K), x)
+    st = load().q4_dispatch(x.data_ptr(), places.data_ptr(), xs.data_ptr(), _TYPE[x.dtype], M, top, K,
+                            handle)
     _check(st, "q4_dispatch")
     return xs
 
@@ -647,14 +654,16 @@ def q4_combine(ys: torch.Tensor, places: torch.Tensor, weights: torch.Tensor = N
     M, top, K = _row_sizes(ys, "ys", places, False)
     if weights is not None:
         _operand(weights, "weights", _F32, (M, top), ys)
-    handle, context = _on(ys, stream)
-    with context:
-        if out is None:
-            out = torch.empty((M, K), dtype=ys.dtype, device=ys.device)
-        else:
-            _operand(out, "out", (ys.dtype,), (M, K), ys)
-        st = load().q4_combine(ys.data_ptr(), places.data_ptr(), None if weights is None else weights.data_ptr(),
-                               out.data_ptr(), _TYPE[ys.dtype], M, top, K, handle)
+    if _elsewhere(ys, stream):
+        with _Foreign(ys.get_device(), stream):
+            return q4_combine(ys, places, weights, out)
+    handle = torch._C._cuda_getCurrentRawStream(ys.get_device())
+    if out is None:
+        out = torch.empty(M, K, dtype=ys.dtype, device=ys.device)
+    else:
+        _operand(out, "out", (ys.dtype,), (M, K), ys)
+    st = load().q4_combine(ys.data_ptr(), places.data_ptr(), None if weights is None else weights.data_ptr(),
+                           out.data_ptr(), _TYPE[ys.dtype], M, top, K, handle)
     _check(st, "q4_combine")
     return out
 
@@ -666,18 +675,20 @@ def q4_combine_grad(dout: torch.Tensor, ys: torch.Tensor, places: torch.Tensor, 
     M, top, K = _row_sizes(ys, "ys", places, False)
     _operand(dout, "dout", (ys.dtype,), (M, K), ys)
     _operand(weights, "weights", _F32, (M, top), ys)
-    handle, context = _on(ys, stream)
-    with context:
-        if dys is None:
-            dys = torch.empty((M * top, K), dtype=ys.dtype, device=ys.device)
-        else:
-            _operand(dys, "dys", (ys.dtype,), (M * top, K), ys)
-        if dweights is None:
-            dweights = torch.empty((M, top), dtype=torch.float32, device=ys.device)
-        else:
-            _operand(dweights, "dweights", _F32, (M, top), ys)
-        st = load().q4_combine_grad(dout.data_ptr(), ys.data_ptr(), places.data_ptr(), weights.data_ptr(),
-                                    dys.data_ptr(), dweights.data_ptr(), _TYPE[ys.dtype], M, top, K, handle)
+    if _elsewhere(ys, stream):
+        with _Foreign(ys.get_device(), stream):
+            return q4_combine_grad(dout, ys, places, weights, dys, dweights)
+    handle = torch._C._cuda_getCurrentRawStream(ys.get_device())
+    if dys is None:
+        dys = torch.empty(M * top, K, dtype=ys.dtype, device=ys.device)
+    else:
+        _operand(dys, "dys", (ys.dtype,), (M * top, K), ys)
+    if dweights is None:
+        dweights = torch.empty(M, top, dtype=torch.float32, device=ys.device)
+    else:
+        _operand(dweights, "dweights", _F32, (M, top), ys)
+    st = load().q4_combine_grad(dout.data_ptr(), ys.data_ptr(), places.data_ptr(), weights.data_ptr(),
+                                dys.data_ptr(), dweights.data_ptr(), _TYPE[ys.dtype], M, top, K, handle)
     _check(st, "q4_combine_grad")
     return dys, dweights
 
