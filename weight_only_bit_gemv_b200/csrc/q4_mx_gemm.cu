@@ -80,8 +80,9 @@ struct Workspace {
 int x_blocks(int tokens, bool pair) { return pair ? 2 : (2 * tokens + kMxBlock - 1) / kMxBlock; }
 
 // Up to 64 tokens an expert: the smallest tile of 8, 16, 32, 64 that holds an
-// expert's average share.  More: pairs of CTAs, and the share in equal tiles of
-// at most 120 tokens.
+// expert's average share.  More: pairs of CTAs, and tiles of at most 120
+// tokens: equal ones for one matrix, of 120 where experts differ (a pair's
+// tile with fewer tokens has shorter MMAs).
 struct Plan {
     int tokens;
     bool pair;
@@ -90,6 +91,7 @@ Plan plan_for(int64_t T, int64_t E) {
     const int64_t share = (T + E - 1) / E;
     for (int t = 8; t <= 64; t *= 2)
         if (share <= t) return {t, false};
+    if (E > 1) return {kPairTokens, true};
     const int64_t tiles = (share + kPairTokens - 1) / kPairTokens;
     return {static_cast<int>(((share + tiles - 1) / tiles + 7) / 8 * 8), true};
 }
@@ -112,6 +114,9 @@ Workspace workspace_layout(int64_t T, int64_t E, int64_t N, int64_t K, const Pla
 // ---------------------------------------------------------------------------
 // x to its two parts, in the order of the token tiles
 // ---------------------------------------------------------------------------
+// Tokens that a pair's MMA computes for a tile of `count`: N has to be a multiple of 16.
+__device__ __forceinline__ int pair_tokens(int count) { return (count + 7) / 8 * 8; }
+
 struct Convert {
     const uint16_t* x;
     const int32_t* rows;  // x row of each of the T rows; nullptr: the row itself
@@ -121,7 +126,7 @@ struct Convert {
     uint32_t* counters;
     void* y;
     int64_t Mx, K, N, counter_count, tile_limit;
-    int T, E, Kb, y_bf16, tokens, x_blocks;
+    int T, E, Kb, y_bf16, tokens, x_blocks, pair;
 };
 
 // One warp converts 256 k of one row: 4 lanes a group of 32, 8 values a lane.
@@ -172,7 +177,8 @@ __global__ void __launch_bounds__(256) convert_kernel(const Convert p) {
         gather_bytes(parts.byte, lane, four, four_lo);
         if ((lane & 15) == 0 && kb < p.Kb) {
             [[maybe_unused]] const int64_t extent = p.tile_limit * p.x_blocks * p.Kb * kMxScaleBytes;
-            const int r = p.tokens + m;
+            // a pair's tile has as many columns as tokens need
+            const int r = (p.pair ? pair_tokens(min(p.tokens, table.offset[e + 1] - (row - m))) : p.tokens) + m;
             const int64_t at = ((tile * p.x_blocks + m / kMxBlock) * p.Kb + kb) * kMxScaleBytes + mx_scale_at(m % kMxBlock, 0);
             const int64_t at_lo =
                 ((tile * p.x_blocks + r / kMxBlock) * p.Kb + kb) * kMxScaleBytes + mx_scale_at(r % kMxBlock, 0);
@@ -221,6 +227,7 @@ struct Shape {
 struct Segment {
     int out;              // output tile
     int e, nt, tile, in;  // expert, row tile, token tile, its number in the expert
+    int first, count;     // its rows of y
     int k0, k1;           // units of k
 };
 // All counts fit 31 bits (the API refuses more units than that).
@@ -251,6 +258,8 @@ struct Runs {
         s.nt = mine == 1 ? local : local / mine;
         s.in = local - s.nt * mine;
         s.tile = t.tile[s.e] + s.in;
+        s.first = t.offset[s.e] + s.in * p.tokens;
+        s.count = min(p.tokens, t.offset[s.e + 1] - s.first);
         return true;
     }
 };
@@ -442,8 +451,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t set = 0;
         bool reused = false;  // the accumulator's earlier contents have to be read first
         const uint64_t adesc = smem_desc_sw128(base, 1024), sdesc = scale_desc(base);
-        const uint32_t idesc = mx_idesc(kMxBlock * kCtas, 2 * tokens, 0);
         while (ok && runs.next(p, table, s)) {
+            const uint32_t idesc = mx_idesc(kMxBlock * kCtas, 2 * (kCtas == 1 ? kTokens : pair_tokens(s.count)), 0);
             for (int k0 = s.k0; ok && k0 < s.k1; k0 += p.flush) {
                 const int k1 = min(s.k1, k0 + p.flush);
                 if (reused && !wait_bar(dempty(dring.slot), dring.parity ^ 1u, abort_flag)) {
@@ -513,6 +522,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         Segment s;
         pdl_wait();  // the counters' zeros, and whoever read the workspace before
         while (ok && runs.next(p, table, s)) {
+            const int cols = kCtas == 1 ? kTokens : pair_tokens(s.count);  // of either part
             float acc[kTokens];
 #pragma unroll
             for (int i = 0; i < kTokens; ++i) acc[i] = 0.0f;
@@ -523,23 +533,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_after();
 #pragma unroll
                 for (int c0 = 0; c0 < kTokens; c0 += kWait) {
-                    if (c0 >= tokens) break;
+                    if (c0 >= cols) break;
                     uint32_t hi[kWait], lo[kWait];
 #pragma unroll
                     for (int c = 0; c < kWait; c += kLoad) {
-                        if (c0 + c >= tokens) break;
+                        if (c0 + c >= cols) break;
                         if constexpr (kLoad == 8) {
                             tc_ld_x8(d + c0 + c, hi + c);
-                            tc_ld_x8(d + tokens + c0 + c, lo + c);
+                            tc_ld_x8(d + cols + c0 + c, lo + c);
                         } else {
                             tc_ld_x32(d + c0 + c, hi + c);
-                            tc_ld_x32(d + tokens + c0 + c, lo + c);
+                            tc_ld_x32(d + cols + c0 + c, lo + c);
                         }
                     }
                     tc_wait_ld();
 #pragma unroll
                     for (int c = 0; c < kWait; c += kLoad) {
-                        if (c0 + c >= tokens) break;
+                        if (c0 + c >= cols) break;
 #pragma unroll
                         for (int i = 0; i < kLoad; ++i)
                             acc[c0 + c + i] += __uint_as_float(hi[c + i]) + __uint_as_float(lo[c + i]);
@@ -557,8 +567,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             ok = epilogue_sync(ok);
             if (!ok) break;
-            const int first = table.offset[s.e] + s.in * tokens;
-            const int count = min(tokens, table.offset[s.e + 1] - first);
+            const int first = s.first, count = s.count;
             const int64_t n0 = (static_cast<int64_t>(s.nt) * kCtas + rank) * kMxBlock, n = n0 + row;
             if (s.k0 == 0 && s.k1 == p.Ku) {
                 // one row of W a thread: a warp's store is 32 outputs of a token in a row
@@ -658,6 +667,7 @@ cudaError_t launch_as(const Plan& plan, const uint8_t* codes, const uint8_t* sca
     c.y_bf16 = y_type == Q4_BF16;
     c.tokens = plan.tokens;
     c.x_blocks = x_blocks(plan.tokens, plan.pair);
+    c.pair = plan.pair;
     const int64_t warps = std::max(T * ((Kb + 1) / 2), (c.counter_count + 255) / 256);
     const int grid = static_cast<int>(std::min<int64_t>((warps + 7) / 8, dev.sm_count * 8));
     if (K % 8 == 0)
