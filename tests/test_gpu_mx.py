@@ -134,7 +134,7 @@ def test_pack_stack_and_guards():
 
 # ---- one matrix -----------------------------------------------------------------
 
-@pytest.mark.parametrize("M", [1, 2, 7, 8, 9, 16, 17, 32, 33, 64, 65, 127, 128, 129, 300])
+@pytest.mark.parametrize("M", [1, 2, 7, 8, 9, 16, 17, 24, 25, 32, 33, 40, 49, 64, 65, 127, 128, 129, 300])
 @pytest.mark.parametrize("N,K", [(1, 1), (200, 130), (384, 1024)])
 def test_gemm(M, N, K):
     rng = np.random.default_rng(M * 1000 + N)

@@ -79,10 +79,12 @@ struct Workspace {
 // Blocks of 128 columns (x rows, hi and lo) whose exponents a tile has.
 int x_blocks(int tokens, bool pair) { return pair ? 2 : (2 * tokens + kMxBlock - 1) / kMxBlock; }
 
-// Up to 64 tokens an expert: the smallest tile of 8, 16, 32, 64 that holds an
-// expert's average share.  More: pairs of CTAs, and tiles of at most 120
-// tokens: equal ones for one matrix, of 120 where experts differ (a pair's
-// tile with fewer tokens has shorter MMAs).
+// Tokens of a tile, and whether pairs of CTAs take it.  Up to 64 tokens an
+// expert one CTA: for one matrix its tokens in whole eights, which are then
+// the MMA's columns; where experts differ, the smallest of 8, 16, 32, 64 that
+// holds their average share.  More: pairs, in tiles of at most 120 tokens:
+// equal ones for one matrix, of 120 where experts differ (a pair's tile with
+// fewer tokens has shorter MMAs).
 struct Plan {
     int tokens;
     bool pair;
@@ -90,7 +92,7 @@ struct Plan {
 Plan plan_for(int64_t T, int64_t E) {
     const int64_t share = (T + E - 1) / E;
     for (int t = 8; t <= 64; t *= 2)
-        if (share <= t) return {t, false};
+        if (share <= t) return {E > 1 ? t : static_cast<int>((share + 7) / 8 * 8), false};
     if (E > 1) return {kPairTokens, true};
     const int64_t tiles = (share + kPairTokens - 1) / kPairTokens;
     return {static_cast<int>(((share + tiles - 1) / tiles + 7) / 8 * 8), true};
@@ -193,8 +195,7 @@ __global__ void __launch_bounds__(256) convert_kernel(const Convert p) {
 // ---------------------------------------------------------------------------
 // the product
 // ---------------------------------------------------------------------------
-// kTokens: of a tile, or for a pair (kCtas = 2) the most a tile may have.  A
-// pair's MMA has 256 rows of W, 128 in each CTA, and reads its columns from
+// kTokens: the most a tile may have.  A pair's (kCtas = 2) MMA has 256 rows of W, 128 in each CTA, and reads its columns from
 // both: the first CTA holds the hi rows of x, the second the lo rows, so each
 // byte of x is brought to one SM for 256 rows of W.
 template <int kTokens, int kCtas>
@@ -312,7 +313,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                    const __grid_constant__ CUtensorMap wsfmap, const __grid_constant__ CUtensorMap xsfmap,
                    const MxGemm p) {
     using S = Shape<kTokens, kCtas>;
-    const int tokens = kCtas == 1 ? kTokens : p.tokens;
+    const int tokens = p.tokens;
     const uint32_t rank = kCtas == 1 ? 0u : cluster_rank();
     const int group = blockIdx.x / kCtas, groups = gridDim.x / kCtas;
     extern __shared__ uint8_t smem_raw[];
@@ -364,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto load_w = [&](int64_t block, int blocks, int slot) {
             const uint32_t dst = base + slot * S::kStagePitch, bar = leader_full + 8u * slot;
             // the load that spreads the nibbles counts the bytes it reads
-            const int brows = kCtas == 1 ? S::kCols : tokens;
+            const int brows = 2 * tokens / kCtas;
             if (rank == 0)
                 mbar_arrive_expect_tx(full(slot), kCtas * (S::kUnit * (kMxCodeBytes + brows * 128) +
                                                            blocks * kMxScaleBytes * (1 + S::kXBlocks)));
@@ -387,7 +388,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                      (tile * S::kXBlocks + b) * p.Kb + kb, bar);
                 return;
             }
-            tma_load_3d(dst + S::kBAt, &xmap, 0, tile * S::kCols, kb, bar);
+            tma_load_3d(dst + S::kBAt, &xmap, 0, 2 * tile * tokens, kb, bar);
 #pragma unroll
             for (int b = 0; b < S::kXBlocks; ++b) {
                 const int64_t at = (static_cast<int64_t>(tile) * S::kXBlocks + b) * p.Kb + kb;
@@ -452,7 +453,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool reused = false;  // the accumulator's earlier contents have to be read first
         const uint64_t adesc = smem_desc_sw128(base, 1024), sdesc = scale_desc(base);
         while (ok && runs.next(p, table, s)) {
-            const uint32_t idesc = mx_idesc(kMxBlock * kCtas, 2 * (kCtas == 1 ? kTokens : pair_tokens(s.count)), 0);
+            const uint32_t idesc = mx_idesc(kMxBlock * kCtas, 2 * (kCtas == 1 ? tokens : pair_tokens(s.count)), 0);
             for (int k0 = s.k0; ok && k0 < s.k1; k0 += p.flush) {
                 const int k1 = min(s.k1, k0 + p.flush);
                 if (reused && !wait_bar(dempty(dring.slot), dring.parity ^ 1u, abort_flag)) {
@@ -488,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                             for (int q = 0; q < 4; ++q)
                                 tc_mma_mx<kCtas>(d, adesc + at + (u * S::kABytes + 32 * q) / 16,
-                                          adesc + at + (S::kBAt + u * S::kBBytes + 32 * q) / 16,
+                                          adesc + at + (S::kBAt + 32 * q) / 16 + u * (2 * tokens / kCtas * 128 / 16),
                                           idesc | mx_idesc(0, 0, q), sfa, sfb, (k > k0 || u > 0 || q > 0) ? 1u : 0u);
                         }
                         tc_commit_all<kCtas>(empty(ring.slot));
@@ -522,7 +523,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         Segment s;
         pdl_wait();  // the counters' zeros, and whoever read the workspace before
         while (ok && runs.next(p, table, s)) {
-            const int cols = kCtas == 1 ? kTokens : pair_tokens(s.count);  // of either part
+            const int cols = kCtas == 1 ? tokens : pair_tokens(s.count);  // of either part
             float acc[kTokens];
 #pragma unroll
             for (int i = 0; i < kTokens; ++i) acc[i] = 0.0f;
@@ -788,9 +789,9 @@ cudaError_t launch_gemm_mx(const uint8_t* codes, const uint8_t* scales, const ui
             return launch_decode_mx(codes, scales, x, rows, offsets, y, y_type, Mx, T, E, N, K, d.split, d.groups, s, dev);
     }
     const auto launch = plan.pair           ? launch_as<kPairTokens, 2>
-                        : plan.tokens == 8  ? launch_as<8, 1>
-                        : plan.tokens == 16 ? launch_as<16, 1>
-                        : plan.tokens == 32 ? launch_as<32, 1> : launch_as<64, 1>;
+                        : plan.tokens <= 8  ? launch_as<8, 1>
+                        : plan.tokens <= 16 ? launch_as<16, 1>
+                        : plan.tokens <= 32 ? launch_as<32, 1> : launch_as<64, 1>;
     return launch(plan, codes, scales, x, rows, offsets, y, y_type, Mx, T, E, N, K, ws, s, dev);
 }
 
