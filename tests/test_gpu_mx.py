@@ -266,7 +266,7 @@ def test_gemm_in_graphs():
     allocated under capture, replayed on two streams at once on new inputs."""
     rng = np.random.default_rng(11)
     made, alive = [], []
-    for M, N, K in ((4, 1000, 3000), (70, 500, 1500)):
+    for M, N, K in ((4, 1000, 3000), (70, 500, 1500), (40, 300, 9000)):
         codes, scales, w = _packed(rng, N, K)
         x = _x(rng, M, K)
         q4.q4_gemm_mx(codes, scales, x, N=N)

@@ -22,8 +22,8 @@
 // columns of one MMA, 128 rows of W its M; the epilogue adds the two halves.
 // An output tile is (expert, 128 rows of W, kTokens tokens) and its K is Kb
 // blocks; all tiles' blocks form one list of units, cut into equal runs, one
-// per persistent CTA, so few tiles still use every SM and there is no tail.
-// Where a tile is cut, each CTA stores its part to the workspace and counts
+// per persistent CTA, so that there is no tail (fewer tiles than CTAs: see
+// Runs).  Where a tile is cut, each CTA stores its part to the workspace and counts
 // itself in; the last to come adds all parts in CTA order, so results do not
 // depend on timing and no CTA waits for another.
 //
@@ -50,7 +50,6 @@ namespace {
 constexpr int kThreads = 192;     // producer, MMA, four epilogue warps
 constexpr int kFlush32 = 8;       // k blocks per accumulation in tensor memory, binary32 y
 constexpr int kFlush16 = 64;      // ... bfloat16 y
-constexpr int kMinBlocks = 4;     // least k blocks a CTA is started for
 constexpr int kPairTokens = 120;  // most tokens of a pair's tile: two accumulators of 240 columns
 
 struct MxGemm {
@@ -67,7 +66,7 @@ struct MxGemm {
     int Nt;                       // row tiles of W: Nb, or pairs of row blocks
     int Ku;                       // units (stages) of k of a tile
     int flush;                    // units per accumulation in tensor memory
-    int min_units;                // least units a CTA is started for
+    float block, join, part;      // us of a k block, of adding a tile's parts up, and of each part (see Runs)
 };
 
 // Layout of the workspace, all parts multiples of 1024 bytes.
@@ -232,11 +231,25 @@ struct Segment {
     int k0, k1;           // units of k
 };
 // All counts fit 31 bits (the API refuses more units than that).
+// With fewer output tiles than groups (CTAs or pairs), as many groups share a
+// tile as make the time least, counted in us: its k blocks at `block` each,
+// divided by the sharers, plus `join` and `part` a sharer for adding the parts
+// up.  With one group a tile nothing is added up.  Measured on B200 (us; equal
+// runs over all groups, whole tiles): 64 tokens, 4096 x 4096 17.1, 13.5; 100
+// tokens 23.4, 15.8; 40 tokens, 2048 x 2048 11.3, 8.9; 12 tokens 11.0, 10.6.
 struct Runs {
     int units, ctas, each, more, u, u1;  // CTAs below `more` take one unit beyond `each`
     __device__ Runs(const MxGemm& p, const Table& t, int c, int groups) {
-        units = min(t.tile[p.E], p.tile_limit) * p.Nt * p.Ku;
-        ctas = min(groups, max(units / p.min_units, 1));
+        const int tiles = min(t.tile[p.E], p.tile_limit) * p.Nt;
+        units = tiles * p.Ku;
+        ctas = max(min(groups, units), 1);
+        if (tiles > 0 && tiles < groups) {
+            const float whole = static_cast<float>(p.Kb) * p.block;
+            const int sharers = min(max(static_cast<int>(sqrtf(whole / p.part)), 1), p.Ku);
+            if (static_cast<float>(tiles) * static_cast<float>(sharers) < static_cast<float>(groups)) ctas = tiles * sharers;
+            const float each_tile = static_cast<float>(ctas) / static_cast<float>(tiles);
+            if (whole <= whole / each_tile + p.join + p.part * each_tile) ctas = tiles;
+        }
         each = units / ctas;
         more = units - each * ctas;
         u = c < ctas ? start(c) : units;
@@ -714,7 +727,10 @@ cudaError_t launch_as(const Plan& plan, const uint8_t* codes, const uint8_t* sca
     p.y_bf16 = c.y_bf16;
     p.Ku = static_cast<int>((Kb + S::kUnit - 1) / S::kUnit);
     p.flush = (c.y_bf16 ? kFlush16 : kFlush32) / S::kUnit;
-    p.min_units = kMinBlocks / S::kUnit;
+
+    p.block = kCtas > 1 ? 0.37f : kTokens > 32 ? 0.27f : 0.19f;
+    p.join = 2.0f + 0.07f * static_cast<float>(plan.tokens);
+    p.part = 0.3f + 0.014f * static_cast<float>(plan.tokens);
     const void* fn = reinterpret_cast<const void*>(gemm_mx_kernel<kTokens, kCtas>);
     constexpr int kSlot = kTokens == 8 ? 100 : kTokens == 16 ? 101 : kTokens == 32 ? 102 : kTokens == 64 ? 103 : 104;
     if (S::kSmem > dev.smem_optin) return cudaErrorNotSupported;
@@ -728,7 +744,7 @@ cudaError_t launch_as(const Plan& plan, const uint8_t* codes, const uint8_t* sca
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg{};
     const int64_t groups = std::min<int64_t>(std::min(dev.sm_count, kMxMaxSms) / kCtas,
-                                             std::max<int64_t>(1, l.tiles * p.Nt * p.Ku / p.min_units));
+                                             std::max<int64_t>(1, l.tiles * p.Nt * p.Ku));
     cfg.gridDim = dim3(static_cast<unsigned>(groups * kCtas));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = S::kSmem;
