@@ -20,6 +20,7 @@ namespace {
 // experts: it goes through the 32 different ids one by one).  Only whole
 // numbers are added atomically, so the result is fixed.  Bound by latency: two
 // passes and three barriers; a warp has kSortBatch rounds of ids in flight.
+// Measured on B200: 24 choices of 8 experts 3.9 us, 131072 of 256 21 us.
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kSortCluster = 8;  // CTAs for more choices than one CTA sorts as fast
@@ -181,7 +182,11 @@ __global__ void __launch_bounds__(kSortThreads)
 // widest type that divides a row, every access a whole warp's.  They are bound
 // by memory: dispatch reads each row of x once for all its copies, combine
 // writes each row of out once, and the gradient reads dout once for all the
-// token's choices.  Places outside [-T, T) are skipped.
+// token's choices.  Places outside [-T, T) are skipped.  Measured on B200,
+// 16384 tokens x 8 of 256, K = 2048 bfloat16: dispatch 98 us (6.2 TB/s), combine
+// 104 us (5.8 TB/s), its gradient 201 us (5.7 TB/s).  (Looking up eight places
+// and holding eight pieces first, for more loads in flight, took 104 to 149 us:
+// fewer threads fit.)
 constexpr int kRowThreads = 256;
 
 // The position a place names, and whether its choice was kept.
