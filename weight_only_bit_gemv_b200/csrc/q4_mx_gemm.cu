@@ -89,19 +89,24 @@ int x_blocks(int tokens, bool pair) { return pair ? 2 : (2 * tokens + kMxBlock -
 
 // Tokens of a tile, and whether pairs of CTAs take it.  Up to 64 tokens an
 // expert one CTA: for one matrix its tokens in whole eights, which are then
-// the MMA's columns; where experts differ, the smallest of 8, 16, 32, 64 that
-// holds their average share.  More: pairs, in tiles of at most 120 tokens:
-// equal ones for one matrix, of 120 where experts differ (a pair's tile with
-// fewer tokens has shorter MMAs).
+// the MMA's columns.  Experts differ, and one with more rows than a tile reads
+// its codes again, which costs more than wider MMAs: their tiles hold twice the
+// average share (64 experts of 2048 x 4096, tiles of the share or of twice:
+// 32 tokens x 8 58 or 51 us, 64 67 or 58 us, 256 102 or 98 us), up to 64 for
+// shares from 17 to 64 (512 tokens: 154 us; pairs 168 us).  More: pairs, in tiles of at most
+// 120 tokens: equal ones for one matrix, of 120 where experts differ (a pair's
+// tile with fewer tokens has shorter MMAs).
 struct Plan {
     int tokens;
     bool pair;
 };
 Plan plan_for(int64_t T, int64_t E) {
     const int64_t share = (T + E - 1) / E;
-    for (int t = 8; t <= 64; t *= 2)
-        if (share <= t) return {E > 1 ? t : static_cast<int>((share + 7) / 8 * 8), false};
-    if (E > 1) return {kPairTokens, true};
+    if (E > 1) {
+        if (share > 64) return {kPairTokens, true};
+        return {share <= 2 ? 8 : share <= 8 ? 16 : share <= 16 ? 32 : 64, false};
+    }
+    if (share <= 64) return {static_cast<int>((share + 7) / 8 * 8), false};
     const int64_t tiles = (share + kPairTokens - 1) / kPairTokens;
     return {static_cast<int>(((share + tiles - 1) / tiles + 7) / 8 * 8), true};
 }
