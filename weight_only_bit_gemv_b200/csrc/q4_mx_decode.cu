@@ -381,13 +381,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int m0 = 0; m0 < kTokens; m0 += 2) {
                 if (m0 >= tokens) break;
-                float v[2][8];
                 XParts parts[2];
                 uint32_t hi[2], lo[2];
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    unpack_x8(q[m0 + j], v[j]);
-                    parts[j] = split_x(v[j]);
+                    parts[j] = split_x(q[m0 + j]);
                     gather_bytes(parts[j].byte, lane, hi[j], lo[j]);
                 }
 #pragma unroll

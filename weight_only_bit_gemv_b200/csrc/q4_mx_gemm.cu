@@ -142,9 +142,10 @@ struct Convert {
     void* y;
     int64_t Mx, K, N, counter_count, tile_limit;
     int T, E, Kb, y_bf16, tokens, x_blocks, pair;
+    int split;  // warps that share a row, a power of two
 };
 
-// One warp converts 256 k of one row: 4 lanes a group of 32, 8 values a lane.
+// A warp converts 256 k of a row at a time: 4 lanes a group of 32, 8 values a lane.
 template <bool kVector>
 __global__ void __launch_bounds__(256) convert_kernel(const Convert p) {
     __shared__ Table table;
@@ -162,11 +163,16 @@ __global__ void __launch_bounds__(256) convert_kernel(const Convert p) {
         else
             static_cast<float*>(p.y)[i] = 0.0f;
     }
+    // A warp takes every p.split-th run of 256 k of a row, kFlight of them at a
+    // time so that their loads are in flight together.
+    constexpr int kFlight = 4;
     const int lane = threadIdx.x & 31;
-    const int pieces = (p.Kb + 1) / 2;  // runs of 256 k
-    const int64_t jobs = static_cast<int64_t>(table.offset[p.E]) * pieces;
-    for (int64_t job = thread / 32; job < jobs; job += threads / 32) {
-        const int row = static_cast<int>(job / pieces), piece = static_cast<int>(job % pieces);
+    const int pieces = (p.Kb + 1) / 2;
+    const int part = static_cast<int>(thread / 32) & (p.split - 1), step = p.split;
+    const int64_t row_step = threads / 32 / p.split;
+    const int64_t Kp = static_cast<int64_t>(p.Kb) * kMxBlock;
+    for (int64_t r = thread / 32 / p.split; r < table.offset[p.E]; r += row_step) {
+        const int row = static_cast<int>(r);
         const int e = find_expert(table.offset, p.E, row);
         const int in = row - table.offset[e];
         const int64_t tile = table.tile[e] + in / p.tokens;
@@ -174,32 +180,43 @@ __global__ void __launch_bounds__(256) convert_kernel(const Convert p) {
         const int m = in % p.tokens;
         const int64_t src = p.rows ? static_cast<int64_t>(__ldg(p.rows + row)) : row;
         const bool have = src >= 0 && src < p.Mx;
-        const int64_t k = piece * 256 + 8 * lane;
-        const int kb = 2 * piece + lane / 16;
-        float v[8];
-        unpack_x8(load_x8<kVector>(p.x, have, src * p.K + k, k, p.K, p.Mx * p.K), v);
-        const XParts parts = split_x(v);
-        if (kb < p.Kb) {
-            const int64_t Kp = static_cast<int64_t>(p.Kb) * kMxBlock;
-            [[maybe_unused]] const int64_t extent = p.tile_limit * 2 * p.tokens * Kp;
-            const int64_t at = (tile * 2 * p.tokens + m) * Kp + k;
-            if (Q4_IN_BOUNDS(at, 8, extent) && Q4_IN_BOUNDS(at + p.tokens * Kp, 8, extent)) {
-                *reinterpret_cast<uint2*>(p.xq + at) = parts.hi;
-                *reinterpret_cast<uint2*>(p.xq + at + p.tokens * Kp) = parts.lo;
+        // the row's hi and lo columns; a pair's tile has as many as tokens need
+        const int lo_m = (p.pair ? pair_tokens(min(p.tokens, table.offset[e + 1] - (row - m))) : p.tokens) + m;
+        const int64_t first = (have ? src : 0) * p.K;
+        for (int p0 = part; p0 < pieces; p0 += step * kFlight) {
+            uint4 q[kFlight];
+#pragma unroll
+            for (int i = 0; i < kFlight; ++i) {
+                const int64_t k = static_cast<int64_t>(p0 + i * step) * 256 + 8 * lane;
+                q[i] = load_x8<kVector>(p.x, have, first + k, k, p.K, p.Mx * p.K);
             }
-        }
-        uint32_t four, four_lo;
-        gather_bytes(parts.byte, lane, four, four_lo);
-        if ((lane & 15) == 0 && kb < p.Kb) {
-            [[maybe_unused]] const int64_t extent = p.tile_limit * p.x_blocks * p.Kb * kMxScaleBytes;
-            // a pair's tile has as many columns as tokens need
-            const int r = (p.pair ? pair_tokens(min(p.tokens, table.offset[e + 1] - (row - m))) : p.tokens) + m;
-            const int64_t at = ((tile * p.x_blocks + m / kMxBlock) * p.Kb + kb) * kMxScaleBytes + mx_scale_at(m % kMxBlock, 0);
-            const int64_t at_lo =
-                ((tile * p.x_blocks + r / kMxBlock) * p.Kb + kb) * kMxScaleBytes + mx_scale_at(r % kMxBlock, 0);
-            if (Q4_IN_BOUNDS(at, 4, extent) && Q4_IN_BOUNDS(at_lo, 4, extent)) {
-                *reinterpret_cast<uint32_t*>(p.xsf + at) = four;
-                *reinterpret_cast<uint32_t*>(p.xsf + at_lo) = four_lo;
+#pragma unroll
+            for (int i = 0; i < kFlight; ++i) {
+                const int piece = p0 + i * step;
+                if (piece >= pieces) break;
+                const int64_t k = static_cast<int64_t>(piece) * 256 + 8 * lane;
+                const int kb = 2 * piece + lane / 16;
+                const XParts parts = split_x(q[i]);
+                uint32_t four, four_lo;
+                gather_bytes(parts.byte, lane, four, four_lo);
+                if (kb >= p.Kb) continue;
+                [[maybe_unused]] const int64_t extent = p.tile_limit * 2 * p.tokens * Kp;
+                const int64_t at = (tile * 2 * p.tokens + m) * Kp + k;
+                if (Q4_IN_BOUNDS(at, 8, extent) && Q4_IN_BOUNDS(at + p.tokens * Kp, 8, extent)) {
+                    *reinterpret_cast<uint2*>(p.xq + at) = parts.hi;
+                    *reinterpret_cast<uint2*>(p.xq + at + p.tokens * Kp) = parts.lo;
+                }
+                if ((lane & 15) != 0) continue;
+                // the four groups of a k block: one 32-bit store per part
+                [[maybe_unused]] const int64_t sf_extent = p.tile_limit * p.x_blocks * p.Kb * kMxScaleBytes;
+                const int64_t sf =
+                    ((tile * p.x_blocks + m / kMxBlock) * p.Kb + kb) * kMxScaleBytes + mx_scale_at(m % kMxBlock, 0);
+                const int64_t sf_lo =
+                    ((tile * p.x_blocks + lo_m / kMxBlock) * p.Kb + kb) * kMxScaleBytes + mx_scale_at(lo_m % kMxBlock, 0);
+                if (Q4_IN_BOUNDS(sf, 4, sf_extent) && Q4_IN_BOUNDS(sf_lo, 4, sf_extent)) {
+                    *reinterpret_cast<uint32_t*>(p.xsf + sf) = four;
+                    *reinterpret_cast<uint32_t*>(p.xsf + sf_lo) = four_lo;
+                }
             }
         }
     }
@@ -696,8 +713,19 @@ cudaError_t launch_as(const Plan& plan, const uint8_t* codes, const uint8_t* sca
     c.tokens = plan.tokens;
     c.x_blocks = x_blocks(plan.tokens, plan.pair);
     c.pair = plan.pair;
-    const int64_t warps = std::max(T * ((Kb + 1) / 2), (c.counter_count + 255) / 256);
-    const int grid = static_cast<int>(std::min<int64_t>((warps + 7) / 8, dev.sm_count * 8));
+    // as many warps to a row as leave each four runs of 256 k, and more where
+    // rows are too few for the SMs
+    const int64_t pieces = (Kb + 1) / 2;
+    c.split = 1;
+    while (c.split < pieces && (pieces > 4 * c.split || T * c.split < 8 * dev.sm_count) && c.split < 1024) c.split *= 2;
+    while (c.split > 1 && T * c.split > 64 * static_cast<int64_t>(dev.sm_count) && pieces < 16 * c.split) c.split /= 2;
+    const int64_t warps = std::max<int64_t>(T * c.split, (c.counter_count + 255) / 256);
+    // whole groups of warps that share rows: 8 warps a block
+    const int64_t most = static_cast<int64_t>(dev.sm_count) * 8;
+    int64_t blocks = std::min<int64_t>((warps + 7) / 8, std::max<int64_t>(most, (c.split + 7) / 8));
+    const int64_t whole = std::max<int64_t>(1, c.split / 8);
+    blocks = (blocks + whole - 1) / whole * whole;
+    const int grid = static_cast<int>(blocks);
     if (K % 8 == 0)
         convert_kernel<true><<<grid, 256, 0, s>>>(c);
     else

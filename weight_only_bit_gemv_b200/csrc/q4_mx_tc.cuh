@@ -264,49 +264,51 @@ __device__ __forceinline__ int find_expert(const int* first, int E, int v) {
 // ---------------------------------------------------------------------------
 // x to its two e4m3 parts
 // ---------------------------------------------------------------------------
-// Eight binary32 values to e4m3 and back.
-__device__ __forceinline__ uint32_t to_e4m3x2(float a, float b) {
+// Two binary16 values to e4m3 (nearest, saturating) and back.
+__device__ __forceinline__ uint32_t to_e4m3x2(__half2 v) {
     uint16_t r;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %2, %1;" : "=h"(r) : "f"(a), "f"(b));
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(*reinterpret_cast<const uint32_t*>(&v)));
     return r;
 }
-__device__ __forceinline__ float2 from_e4m3x2(uint32_t v) {
+__device__ __forceinline__ __half2 from_e4m3x2(uint32_t v) {
     uint32_t h;
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(v)));
-    return __half22float2(*reinterpret_cast<const __half2*>(&h));
+    return *reinterpret_cast<const __half2*>(&h);
 }
-
 
 // A lane's eight consecutive x of a row, a group of 32 in four lanes, as the
 // two parts and hi's exponent byte; 255, the byte of NaN, for a group with an
-// infinity or NaN.
+// infinity or NaN.  x / s is exact in bfloat16 (a power of two), and in
+// binary16 from 2^-17 on; what is smaller goes to zero in both parts, being
+// below half of lo's smallest step, 2^-15.  The remainder x / s - hi has at
+// most 8 bits, so two values at a time in binary16 lose nothing.
 struct XParts {
     uint2 hi, lo;
     uint32_t byte;
 };
-__device__ __forceinline__ XParts split_x(const float (&v)[8]) {
-    uint32_t top = 0;
+__device__ __forceinline__ XParts split_x(const uint4& q) {
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+    uint32_t both = 0;  // magnitudes order as their bits do
 #pragma unroll
-    for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+    for (int j = 0; j < 4; ++j) both = __vmaxu2(both, w[j] & 0x7FFF7FFFu);
+    uint32_t top = max(both & 0xFFFFu, both >> 16);
     top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
     top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
     // the largest value's exponent field - 7, so that the largest x / s is in
     // [128, 256); at least 5, which leaves lo's byte >= 0
-    const uint32_t field = top >> 23;
+    const uint32_t field = top >> 7;
     const uint32_t byte = field > 12u ? field - 7u : 5u;
-    const float inverse = __uint_as_float((254u - byte) << 23);
-    uint32_t h[2], l[2];
+    const uint32_t inverse = ((254u - byte) << 7) * 0x10001u;
+    uint32_t h[2] = {0, 0}, l[2] = {0, 0};
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        h[j] = l[j] = 0;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const float a = v[4 * j + 2 * i] * inverse, b = v[4 * j + 2 * i + 1] * inverse;
-            const uint32_t c = to_e4m3x2(a, b);
-            const float2 back = from_e4m3x2(c);
-            h[j] |= c << (16 * i);
-            l[j] |= to_e4m3x2((a - back.x) * 32.0f, (b - back.y) * 32.0f) << (16 * i);
-        }
+    for (int j = 0; j < 4; ++j) {
+        const __nv_bfloat162 scaled = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&w[j]),
+                                              *reinterpret_cast<const __nv_bfloat162*>(&inverse));
+        const __half2 a = __float22half2_rn(__bfloat1622float2(scaled));
+        const uint32_t c = to_e4m3x2(a);
+        const __half2 rest = __hmul2(__hsub2(a, from_e4m3x2(c)), __float2half2_rn(32.0f));
+        h[j / 2] |= c << (16 * (j & 1));
+        l[j / 2] |= to_e4m3x2(rest) << (16 * (j & 1));
     }
     return {make_uint2(h[0], h[1]), make_uint2(l[0], l[1]), field == 255u ? 255u : byte};
 }
@@ -339,14 +341,6 @@ __device__ __forceinline__ uint4 load_x8(const uint16_t* __restrict__ x, bool ha
         if (have && k + j < K && Q4_IN_BOUNDS(first + j, 1, extent))
             w[j / 2] |= static_cast<uint32_t>(x[first + j]) << (16 * (j & 1));
     return q;
-}
-__device__ __forceinline__ void unpack_x8(const uint4& q, float (&v)[8]) {
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        v[2 * j] = __uint_as_float(w[j] << 16);
-        v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
-    }
 }
 
 }  // namespace
