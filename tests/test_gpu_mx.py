@@ -156,7 +156,7 @@ def test_gemm_long_and_wide(M, N, K):
     _close(q4.q4_gemm_mx(codes, scales, x, N=N, dtype=torch.bfloat16), w, x)
 
 
-@pytest.mark.parametrize("M", [1, 3, 8])
+@pytest.mark.parametrize("M", [1, 3, 8, 13])
 @pytest.mark.parametrize("N,K", [(128, 3000), (130, 1500), (5000, 1408), (4096, 4096), (128, 11008), (20000, 2304), (18900, 4224)])
 def test_gemm_few_tokens(M, N, K):
     """Every split of K over a tile's thread blocks, rings that go round many

@@ -1,5 +1,5 @@
-// q4_mx_decode.cu -- products with microscaled matrices for at most 8 tokens a
-// tile (decode): one launch, no workspace.
+// q4_mx_decode.cu -- products with microscaled matrices in tiles of 8 tokens, for
+// decode: one launch, no workspace.
 //
 // The mathematics is q4_mx_gemm.cu's: hi and lo rows of 8 tokens are the 16
 // columns of one block-scaled MMA.  What differs is who prepares x and who

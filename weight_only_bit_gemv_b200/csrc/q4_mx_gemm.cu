@@ -93,9 +93,9 @@ int x_blocks(int tokens, bool pair) { return pair ? 2 : (2 * tokens + kMxBlock -
 // its codes again, which costs more than wider MMAs: their tiles hold twice the
 // average share (64 experts of 2048 x 4096, tiles of the share or of twice:
 // 32 tokens x 8 58 or 51 us, 64 67 or 58 us, 256 102 or 98 us), up to 64 for
-// shares from 17 to 64 (512 tokens: 154 us; pairs 168 us).  More: pairs, in tiles of at most
-// 120 tokens: equal ones for one matrix, of 120 where experts differ (a pair's
-// tile with fewer tokens has shorter MMAs).
+// shares from 17 to 64 (512 tokens: 154 us; pairs 168 us).  More: pairs, in
+// tiles of at most 120 tokens: equal ones for one matrix, of 120 where experts
+// differ (a pair's tile with fewer tokens has shorter MMAs).
 struct Plan {
     int tokens;
     bool pair;
@@ -225,9 +225,10 @@ __global__ void __launch_bounds__(256) convert_kernel(const Convert p) {
 // ---------------------------------------------------------------------------
 // the product
 // ---------------------------------------------------------------------------
-// kTokens: the most a tile may have.  A pair's (kCtas = 2) MMA has 256 rows of W, 128 in each CTA, and reads its columns from
-// both: the first CTA holds the hi rows of x, the second the lo rows, so each
-// byte of x is brought to one SM for 256 rows of W.
+// kTokens: the most a tile may have.  A pair's (kCtas = 2) MMA has 256 rows of
+// W, 128 in each CTA, and reads its columns from both: the first CTA holds the
+// hi rows of x, the second the lo rows, so each byte of x is brought to one SM
+// for 256 rows of W.
 template <int kTokens, int kCtas>
 struct Shape {
     static constexpr int kCols = 2 * kTokens;                    // MMA N
@@ -798,12 +799,13 @@ cudaError_t launch_as(const Plan& plan, const uint8_t* codes, const uint8_t* sca
 
 }  // namespace
 
-// Whether a product with tiles of 8 tokens runs on q4_mx_decode.cu, and how:
-// the CTAs that share a tile's K (0: not at all), and how many such groups.
+// Whether a product of few tokens runs on q4_mx_decode.cu, in tiles of 8, and
+// how: the CTAs that share a tile's K (0: not at all), and how many such groups.
 // Counted in stages of 256 k, 0.31 us each on one SM (0.42 us with more than 4
 // tokens, whose x takes longer to prepare than the codes to come): a turn of a
 // group costs half a stage beside its own, sharing a tile 5 stages once, and
-// the kernel above 21 for its second launch and its sums' way through memory.
+// the kernel above 21 for its second launch and its sums' way through memory,
+// 30 from 9 to 16 tokens, where the decode kernel reads the codes twice.
 // Measured on B200 (us, 1 token; 1, 2, 4 CTAs a tile; the kernel above):
 //   4096 x 4096   8.0  6.8  5.8;  9.5     28672 x 4096  14.9 16.1 14.4; 17.7
 //   4096 x 14336 21.0 13.5 10.0; 12.1     28672 x 8192  26.0 27.6 24.4; 26.6
@@ -811,11 +813,15 @@ cudaError_t launch_as(const Plan& plan, const uint8_t* codes, const uint8_t* sca
 struct DecodePlan {
     int split, groups;
 };
-static DecodePlan decode_plan(int64_t tiles, int64_t Kb, int64_t share) {
-    const int64_t Ku = (Kb + 1) / 2;
-    const double stage = share > 4 ? 1.35 : 1.0;
+static DecodePlan decode_plan(int64_t T, int64_t E, int64_t N, int64_t K, const Plan& plan) {
     DecodePlan best{0, 0};
-    double least = static_cast<double>(tiles) * Ku / 148 + 21.0;
+    const int64_t share = (T + E - 1) / E;
+    if (share > 16 || (E > 1 && plan.tokens > 8)) return best;
+    const int64_t Nb = mx_blocks(N), Ku = (mx_blocks(K) + 1) / 2;
+    const int64_t tiles = workspace_layout(T, E, N, K, {8, false}).tiles * Nb;  // of 8 tokens
+    const int64_t above = E > 1 ? tiles : Nb;                                    // the kernel above's
+    const double stage = share > 4 ? 1.35 : 1.0;
+    double least = static_cast<double>(above) * Ku / 148 + (share > 8 ? 30.0 : 21.0);
     for (int split = 1; split <= 4; split *= 2) {
         const int most = split == 1 ? 148 : split == 2 ? 74 : 33;  // groups that run at once
         const int64_t turns = (tiles + most - 1) / most;
@@ -832,7 +838,7 @@ int64_t gemm_mx_workspace(int64_t T, int64_t E, int64_t N, int64_t K) {
     const Plan plan = plan_for(T, E);
     const Workspace l = workspace_layout(T, E, N, K, plan);
     if (l.tiles > INT32_MAX / (mx_blocks(N) * mx_blocks(K))) return -1;
-    if (plan.tokens == 8 && decode_plan(l.tiles * mx_blocks(N), mx_blocks(K), (T + E - 1) / E).split > 0) return 0;
+    if (decode_plan(T, E, N, K, plan).split > 0) return 0;
     return static_cast<int64_t>(l.bytes);
 }
 
@@ -841,11 +847,9 @@ cudaError_t launch_gemm_mx(const uint8_t* codes, const uint8_t* scales, const ui
                            int64_t K, void* workspace, cudaStream_t s, const DeviceInfo& dev) {
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     const Plan plan = plan_for(T, E);
-    if (plan.tokens == 8) {
-        const DecodePlan d = decode_plan(workspace_layout(T, E, N, K, plan).tiles * mx_blocks(N), mx_blocks(K), (T + E - 1) / E);
-        if (d.split > 0)
-            return launch_decode_mx(codes, scales, x, rows, offsets, y, y_type, Mx, T, E, N, K, d.split, d.groups, s, dev);
-    }
+    const DecodePlan d = decode_plan(T, E, N, K, plan);
+    if (d.split > 0)
+        return launch_decode_mx(codes, scales, x, rows, offsets, y, y_type, Mx, T, E, N, K, d.split, d.groups, s, dev);
     const auto launch = plan.pair           ? launch_as<kPairTokens, 2>
                         : plan.tokens <= 8  ? launch_as<8, 1>
                         : plan.tokens <= 16 ? launch_as<16, 1>
