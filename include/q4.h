@@ -361,11 +361,26 @@ q4_status q4_dequant_mx(const uint8_t* codes, const uint8_t* scales, void* w_out
  * q4_gemm_mx -- y[m][n] = sum_k W[n][k] x[m][k] for any M >= 0, W microscaled,
  * x bfloat16, y binary32 (Q4_F32) or bfloat16 (Q4_BF16, one rounding), fully
  * overwritten.  Runs on the block-scaled tensor-core instructions, which take
- * codes and exponents as stored; x is split into two 8-bit parts whose sum is
- * x to within 2^-22 of the largest |x| of each 32 (exactly, wherever |x| is
- * at least 2^-14 of it), products are exact and sums binary32.  Within 1e-4 * sum_k |W x| + 1e-6 of the exact sum, and for
- * a given device and shape the same bits on every run.  Input domain: x
- * finite; a row of x that holds an infinity or NaN gives a row of NaN.
+ * codes and exponents as stored; for a given device and shape the same bits on
+ * every run.  Input domain: x finite; a row of x that holds an infinity or NaN
+ * gives a row of NaN.
+ *
+ * Accuracy.  x is split into two 8-bit parts with a scale for each 32 k of a
+ * row: an x of at least 2^-14 of the largest |x| of its 32 is held exactly, a
+ * smaller one to within 2^-22 of that largest.  Products are exact; the tensor
+ * core cuts its sums to binary32, and they are read out and added up in
+ * binary32 every 1024 k, for Q4_BF16 up to every 8192.  With
+ *     S = sum_k |W[n][k] x[m][k]|
+ *     D = sum over groups of 32 k of (largest |x|) * sum |W[n][k]|
+ * y is within 1e-4 * S + 2^-22 * D of the exact sum for Q4_F32 (1.3e-4 * S for
+ * K above 2^18), and within 5.2e-4 * S + 2^-22 * D before its rounding for
+ * Q4_BF16, beside what is below the smallest normal binary32.
+ * D belongs to groups in which some x is below 2^-14 of the largest, and shows
+ * where W is zero or small at that largest: next to an x 2^15 times as large the
+ * others keep 7 bits or more, next to 2^20 times 2 bits, next to 2^24 times
+ * nothing.  Pass a row with such spikes as two rows, the spikes and the rest,
+ * each with zeros in the other's places, and add their results: both are then
+ * exact to the first term.
  *
  * q4_gemm_experts -- the same for rows grouped by expert, W a stack of E
  * matrices: y[p][n] = sum_k W[e][n][k] x[rows[p]][k] for offsets[e] <= p <

@@ -521,7 +521,12 @@ def q4_gemm_mx(codes: torch.Tensor, scales: torch.Tensor, x: torch.Tensor, y: to
     y float32 or bfloat16 (y's type, or ``dtype``).  N defaults to whole
     blocks.  ``workspace`` (uint8, at least q4_gemm_mx_workspace bytes) is
     allocated if not given; one that is given must not be shared by calls
-    that may overlap."""
+    that may overlap.
+
+    x is held to 2^-22 of the largest |x| of each 32 k of a row, exactly where
+    it is at least 2^-14 of that (the bound on y is in include/q4.h): rows in
+    which a few x are more than 2^14 times their neighbours are better passed as
+    two, the large x and the rest, and their results added."""
     _dims(x, "x", (2,), "[M, K]")
     M, K = x.shape
     E, N, K = _mx_sizes(codes, scales, N, K)

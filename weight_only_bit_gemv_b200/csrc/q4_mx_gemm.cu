@@ -11,12 +11,25 @@
 //     lo = e4m3((x / s - hi) * 32),    x = s * hi + (s / 32) * lo.
 // hi takes the leading 4 significant bits, and the remainder's bits fit lo
 // exactly wherever |x| >= 2^-14 of the group's largest; a smaller x is off by
-// at most half of lo's smallest step, 2^-15 s or 2^-22 of that largest.  Products are exact.  The tensor core
+// at most half of lo's smallest step, 2^-15 s or 2^-22 of that largest.  (A
+// third part would hold five octaves more, for half as many MMAs again.  In
+// normally distributed x one element in 17,000 is off at all.  It shows where
+// W is zero or small at a spike of the group; the caller can split such a row
+// exactly, see q4.h.)
+// Products are exact.  The tensor core
 // adds them to its binary32 accumulator by truncation: measured, the relative
 // error grows by 7e-8 for each 128 k.  For a binary32 y the accumulator is
 // therefore read out every kFlush32 blocks of k and added up in registers,
 // rounded to nearest (5e-7 measured at K = 1024); a bfloat16 y, whose own
 // rounding is 2^-9, takes kFlush16 blocks at a time.
+// The bound on y.  A step of 32 k adds 32 products to the accumulator, aligned
+// to the largest of the 33 and cut below 2^-24 of it: 33 * 2^-24 S, S = sum
+// |W x|, for 32 steps a reading (binary32 y) or 256 (bfloat16).  Readings are
+// added in binary32, 2^-24 S each, K / 1024 or K / 8192 of them, hi and lo
+// once more, and at most 64 parts of a tile.  That is (1056 + K / 1024 + 66)
+// 2^-24 S, 8.2e-5 S up to K = 2^18 and 1.3e-4 S at 2^20; for bfloat16
+// (8448 + K / 8192 + 66) 2^-24 S, 5.2e-4 S at 2^20.  The split adds 2^-22 of
+// its group's largest |x| times sum |W| for each group.
 //
 // Work.  The hi rows and lo rows of kTokens tokens are the N = 2 kTokens
 // columns of one MMA, 128 rows of W its M; the epilogue adds the two halves.
