@@ -417,6 +417,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // -------------------------------- teardown --------------------------------
     // The MMAs waited for every load, so none is in flight here unless a wait
     // ran out; then the loads have had the wait's two seconds.
+    __syncwarp();  // a role may have left its loop lane by lane
     tc_fence_before();
     __syncthreads();
     if (kSplit > 1) cluster_sync();  // no CTA's memory goes while another may use it

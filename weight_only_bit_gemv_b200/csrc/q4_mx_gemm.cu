@@ -586,7 +586,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int i = 0; i < kTokens; ++i) acc[i] = 0.0f;
             for (int k0 = s.k0; k0 < s.k1; k0 += p.flush) {
-                ok = __all_sync(0xFFFFFFFFu, wait_bar(dfull(dring.slot), dring.parity, abort_flag));
+                ok = wait_bar(dfull(dring.slot), dring.parity, abort_flag);
                 if (!ok) break;
                 const uint32_t d = lanes + dring.slot * S::kCols;
                 tc_fence_after();
@@ -690,6 +690,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 
     // -------------------------------- teardown --------------------------------
+    __syncwarp();  // a role may have left its loop lane by lane
     pdl_wait();  // no CTA ends before the conversion has: it writes y's last rows
     tc_fence_before();
     __syncthreads();

@@ -6,6 +6,7 @@
 
 #include "q4_mx.cuh"
 #include "q4_sm100.cuh"
+#include "q4_wait.cuh"
 
 namespace q4 {
 namespace {
@@ -143,15 +144,14 @@ __device__ __forceinline__ bool elect_one() {
     return r != 0u;
 }
 
-// mbar_wait that also gives up once another role has.
+// mbar_wait for a whole warp, which also gives up once another role has.  The
+// result is the same in all lanes.
 __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag) {
-    if (mbar_try_wait(bar, parity)) return true;
+    const auto all = [](bool b) { return __all_sync(0xFFFFFFFFu, b) != 0; };
+    if (all(mbar_try_wait(bar, parity))) return true;
     const unsigned long long t0 = globaltimer_ns();
-    while (true) {
-        for (int i = 0; i < 64; ++i)
-            if (mbar_try_wait(bar, parity)) return true;
-        if (*abort_flag || globaltimer_ns() - t0 > kWaitLimitNs) return false;
-    }
+    return wait_together([&] { return mbar_try_wait(bar, parity); },
+                         [&] { return *abort_flag != 0u || globaltimer_ns() - t0 > kWaitLimitNs; }, all);
 }
 
 // A ring's slot and the parity of its use, without divisions.
