@@ -51,6 +51,7 @@ constexpr int kSmem = 1024 + kTailAt + 256;
 constexpr uint32_t kScaleCol = 2 * kCols;                    // after two accumulators, two sets of exponents
 constexpr uint32_t kScaleSet = 8 * kUnit;
 constexpr uint32_t kDecodeCols = 64;
+constexpr unsigned long long kSumsLandNs = 1000000;          // a store to another CTA's shared memory takes about 1 us
 static_assert(kStagePitch % 1024 == 0 && kScaleCol + 2 * kScaleSet <= kDecodeCols, "layout");
 
 struct MxDecode {
@@ -158,6 +159,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         Turns turns(p, table, group, groups);
         Tile s;
         Ring<kStages> ring;
+        int64_t issued = 0;
         while (ok && turns.take(p, table, s)) {
             const int64_t block = (static_cast<int64_t>(s.e) * p.Nb + s.nb) * p.Kb;
             for (int k = k_begin; k < k_end; ++k) {
@@ -174,6 +176,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         bulk_load(dst + kSfaAt, p.wsf + (block + kb) * kMxScaleBytes, blocks * kMxScaleBytes, bar);
                 }
                 __syncwarp();
+                ++issued;
                 ring.next();
                 if (ring.slot == 0) filled = true;
             }
@@ -182,6 +185,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             atomicOr(&g_decode_mx_error, 1u);
             *abort_flag = 1;
         }
+        // Leave only once every copy issued has landed.  After an error in any
+        // role a stage may stay without its x, and the wait then ends by its
+        // limit, which is far longer than a copy takes.
+        for (int64_t i = issued > kStages ? issued - kStages : 0; i < issued; ++i)
+            if (!mbar_wait(full(static_cast<int>(i % kStages)), static_cast<uint32_t>(i / kStages) & 1u)) break;
     } else if (warp == 1) {
         // -------------------------------- MMA ---------------------------------
         bool ok = true, reused = false;
@@ -415,12 +423,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 
     // -------------------------------- teardown --------------------------------
-    // The MMAs waited for every load, so none is in flight here unless a wait
-    // ran out; then the loads have had the wait's two seconds.
     __syncwarp();  // a role may have left its loop lane by lane
     tc_fence_before();
     __syncthreads();
-    if (kSplit > 1) cluster_sync();  // no CTA's memory goes while another may use it
+    if (kSplit > 1) {
+        cluster_sync();  // no CTA's memory goes while another may use it
+        // A first CTA that gave up has not waited for the others' sums, of which
+        // the last may still be on their way to it.
+        if (rank == 0 && *abort_flag != 0u) {
+            const unsigned long long t0 = globaltimer_ns();
+            while (globaltimer_ns() - t0 < kSumsLandNs) {
+            }
+        }
+    }
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem, kDecodeCols);
