@@ -494,10 +494,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             atomicOr(&g_gemm_mx_error, 1u);
             *abort_flag = 1;
         }
-        // leave only once every copy issued has landed (bounded); a pair's
-        // second CTA leaves after the first, at the cluster's barrier below
-        for (int64_t i = rank != 0 ? issued : issued > S::kStages ? issued - S::kStages : 0; i < issued; ++i)
-            if (!mbar_wait(full(static_cast<int>(i % S::kStages)), static_cast<uint32_t>(i / S::kStages) & 1u)) break;
+        // Leave only once every copy issued has landed and, in a pair's second
+        // CTA, the first one's arrivals for its stages have come: they are
+        // sent into this CTA's shared memory.  (Bounded, and without the error
+        // flag, so that an error leaves them time.)
+        for (int64_t i = issued > S::kStages ? issued - S::kStages : 0; i < issued; ++i) {
+            const int slot = static_cast<int>(i % S::kStages);
+            if (!mbar_wait(rank == 0 ? full(slot) : empty(slot), static_cast<uint32_t>(i / S::kStages) & 1u)) break;
+        }
     } else if (warp == 1 && rank != 0) {
         // the pair's first CTA issues for both
     } else if (warp == 1) {
