@@ -66,9 +66,9 @@ int main(int argc, char** argv) {
                 const auto ready = [&] { return ++looks > ready_at[i]; };
                 const auto expired = [&] { return ++asked >= expired_at[i]; };
                 if (together)
-                    result[i] = q4::wait_together(ready, expired, [&](bool b) { return vote(b); });
+                    result[i] = q4::wait_together([&] { return vote(ready()); }, [&] { return !vote(!expired()); });
                 else  // each lane for itself
-                    result[i] = q4::wait_together(ready, expired, [](bool b) { return b; });
+                    result[i] = q4::wait_together(ready, expired);
             });
         for (auto& t : lanes) t.join();
         bool same = true;
@@ -109,8 +109,8 @@ def test_the_trials_part_lanes_that_wait_each_for_itself(program):
 
 
 def test_the_products_wait_as_warps():
-    """wait_bar, which every role of both kernels waits with, takes the vote."""
+    """wait_bar, which every role of both kernels waits with, asks only by votes."""
     text = open(os.path.join(CSRC, "q4_mx_tc.cuh")).read()
-    body = text[text.index("bool wait_bar("):]
-    body = body[:body.index("\n}\n")]
-    assert "wait_together(" in body and "__all_sync(0xFFFFFFFFu" in body
+    body = text[text.index("bool try_wait_all("):text.index("struct Ring")]
+    assert "vote.sync.all.pred q, p, 0xFFFFFFFF" in body and "__any_sync(0xFFFFFFFFu" in body
+    assert "mbar_try_wait(" not in body and "mbar_wait(" not in body

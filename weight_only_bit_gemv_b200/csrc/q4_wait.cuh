@@ -10,17 +10,17 @@
 
 namespace q4 {
 
-// True once `ready` is true in every lane, false once `expired` is in any: the
-// same in all lanes.  One lane may see an error flag or the time limit while
-// another sees the phase complete, and what follows a wait are instructions of
-// the whole warp (elect.sync, tcgen05.ld, __syncwarp), so lanes must not part
-// here.  all(b): whether b is true in every lane, a vote of the warp.
-template <typename Ready, typename Expired, typename All>
-Q4_HOST_DEVICE bool wait_together(Ready ready, Expired expired, All all) {
+// True once `ready`, false once `expired`, both votes of the warp: whether the
+// phase is complete for every lane, and whether the wait is over for any.  One
+// lane may see an error flag or the time limit while another sees the phase
+// complete, and what follows a wait are instructions of the whole warp
+// (elect.sync, tcgen05.ld, __syncwarp), so lanes must not part here.
+template <typename Ready, typename Expired>
+Q4_HOST_DEVICE bool wait_together(Ready ready, Expired expired) {
     while (true) {
         for (int i = 0; i < 64; ++i)
-            if (all(ready())) return true;
-        if (!all(!expired())) return false;
+            if (ready()) return true;
+        if (expired()) return false;
     }
 }
 
