@@ -153,13 +153,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const uint32_t tmem = *word;
 
+    int issued = 0;  // stages that the producer has asked for
+
     if (warp == 0) {
         // ------------------------------ producer ------------------------------
         bool ok = true, filled = false;
         Turns turns(p, table, group, groups);
         Tile s;
         Ring<kStages> ring;
-        int64_t issued = 0;
         while (ok && turns.take(p, table, s)) {
             const int64_t block = (static_cast<int64_t>(s.e) * p.Nb + s.nb) * p.Kb;
             for (int k = k_begin; k < k_end; ++k) {
@@ -185,11 +186,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             atomicOr(&g_decode_mx_error, 1u);
             *abort_flag = 1;
         }
-        // Leave only once every copy issued has landed.  After an error in any
-        // role a stage may stay without its x, and the wait then ends by its
-        // limit, which is far longer than a copy takes.
-        for (int64_t i = issued > kStages ? issued - kStages : 0; i < issued; ++i)
-            if (!mbar_wait(full(static_cast<int>(i % kStages)), static_cast<uint32_t>(i / kStages) & 1u)) break;
     } else if (warp == 1) {
         // -------------------------------- MMA ---------------------------------
         bool ok = true, reused = false;
@@ -423,14 +419,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 
     // -------------------------------- teardown --------------------------------
+    // The MMAs waited for every load and the first CTA for the others' sums, so
+    // nothing is in flight here unless some role gave up.  Then the producer
+    // waits for its last stages (one without its x ends by the limit, which is
+    // far longer than a copy takes), and a first CTA stays until what was still
+    // on its way to it has landed.
     __syncwarp();  // a role may have left its loop lane by lane
     tc_fence_before();
     __syncthreads();
+    const bool gave_up = *abort_flag != 0u;
+    if (gave_up && warp == 0)
+        for (int i = max(issued - kStages, 0); i < issued; ++i)
+            if (!mbar_wait(full(i % kStages), static_cast<uint32_t>(i / kStages) & 1u)) break;
+    __syncwarp();
     if (kSplit > 1) {
         cluster_sync();  // no CTA's memory goes while another may use it
-        // A first CTA that gave up has not waited for the others' sums, of which
-        // the last may still be on their way to it.
-        if (rank == 0 && *abort_flag != 0u) {
+        if (gave_up && rank == 0) {
             const unsigned long long t0 = globaltimer_ns();
             while (globaltimer_ns() - t0 < kSumsLandNs) {
             }
