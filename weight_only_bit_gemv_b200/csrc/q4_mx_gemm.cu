@@ -36,7 +36,7 @@
 // An output tile is (expert, 128 rows of W, kTokens tokens) and its K is Kb
 // blocks; all tiles' blocks form one list of units, cut into equal runs, one
 // per persistent CTA, so that there is no tail (fewer tiles than CTAs: see
-// Runs).  Where a tile is cut, each CTA stores its part to the workspace and counts
+// q4_mx_runs.cuh).  Where a tile is cut, each CTA stores its part to the workspace and counts
 // itself in; the last to come adds all parts in CTA order, so results do not
 // depend on timing and no CTA waits for another.
 //
@@ -61,6 +61,7 @@
 // drains its copies, frees its tensor memory and exits.
 #include <algorithm>
 
+#include "q4_mx_runs.cuh"
 #include "q4_mx_tc.cuh"
 
 namespace q4 {
@@ -88,7 +89,7 @@ struct MxGemm {
     int Nt;                       // row tiles of W: Nb, or pairs of row blocks
     int Ku;                       // units (stages) of k of a tile
     int flush;                    // units per accumulation in tensor memory
-    float block, join, part;      // us of a k block, of adding a tile's parts up, and of each part (see Runs)
+    RunCost cost;
 };
 
 // Layout of the workspace, all parts multiples of 1024 bytes.
@@ -276,35 +277,13 @@ struct Segment {
     int k0, k1;           // units of k
 };
 // All counts fit 31 bits (the API refuses more units than that).
-// With fewer output tiles than groups (CTAs or pairs), as many groups share a
-// tile as make the time least, counted in us: its k blocks at `block` each,
-// divided by the sharers, plus `join` and `part` a sharer for adding the parts
-// up.  With one group a tile nothing is added up.  Measured on B200 (us; equal
-// runs over all groups, whole tiles): 64 tokens, 4096 x 4096 17.1, 13.5; 100
-// tokens 23.4, 15.8; 40 tokens, 2048 x 2048 11.3, 8.9; 12 tokens 11.0, 10.6.
 struct Runs {
-    int units, ctas, each, more, u, u1;  // CTAs below `more` take one unit beyond `each`
-    __device__ Runs(const MxGemm& p, const Table& t, int c, int groups) {
-        const int tiles = min(t.tile[p.E], p.tile_limit) * p.Nt;
-        units = tiles * p.Ku;
-        ctas = max(min(groups, units), 1);
-        if (tiles > 0 && tiles < groups) {
-            const float whole = static_cast<float>(p.Kb) * p.block;
-            const int sharers = min(max(static_cast<int>(sqrtf(whole / p.part)), 1), p.Ku);
-            if (static_cast<float>(tiles) * static_cast<float>(sharers) < static_cast<float>(groups)) ctas = tiles * sharers;
-            const float each_tile = static_cast<float>(ctas) / static_cast<float>(tiles);
-            if (whole <= whole / each_tile + p.join + p.part * each_tile) ctas = tiles;
-        }
-        each = units / ctas;
-        more = units - each * ctas;
-        u = c < ctas ? start(c) : units;
-        u1 = c < ctas ? start(c + 1) : units;
-    }
-    __device__ int start(int c) const { return each * c + min(c, more); }
-    // the CTA whose run holds unit v
-    __device__ int owner(int v) const {
-        const int longer = more * (each + 1);
-        return v < longer ? v / (each + 1) : more + (v - longer) / each;
+    RunCut cut;
+    int u, u1;
+    __device__ Runs(const MxGemm& p, const Table& t, int c, int groups)
+        : cut(min(t.tile[p.E], p.tile_limit) * p.Nt, groups, p.Ku, p.cost) {
+        u = c < cut.ctas ? cut.start(c) : cut.units;
+        u1 = c < cut.ctas ? cut.start(c + 1) : cut.units;
     }
     __device__ bool next(const MxGemm& p, const Table& t, Segment& s) {
         if (u >= u1) return false;
@@ -654,7 +633,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (m < count) __stcg(mine + m * kMxBlock, acc[m]);
             __threadfence();
             epilogue_sync(true);
-            const int u0 = s.out * p.Ku, c0 = runs.owner(u0), c1 = runs.owner(u0 + p.Ku - 1);
+            const int u0 = s.out * p.Ku, c0 = runs.cut.owner(u0), c1 = runs.cut.owner(u0 + p.Ku - 1);
             if (tid == 64) word[2] = atomicAdd(p.counters + s.out * kCtas + rank, 1u) == static_cast<uint32_t>(c1 - c0) ? 1u : 0u;
             epilogue_sync(true);
             if (word[2] == 0u) continue;
@@ -669,7 +648,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int b = 0; b < kBatch; ++b) sum[b] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 2
                 for (int c = c0; c <= c1; ++c) {
-                    const float* part = slot_of(c, runs.start(c) > u0) + 4 * lane;
+                    const float* part = slot_of(c, runs.cut.start(c) > u0) + 4 * lane;
                     float4 v[kBatch];
 #pragma unroll
                     for (int b = 0; b < kBatch; ++b)
@@ -789,9 +768,9 @@ cudaError_t launch_as(const Plan& plan, const uint8_t* codes, const uint8_t* sca
     p.Ku = static_cast<int>((Kb + S::kUnit - 1) / S::kUnit);
     p.flush = (c.y_bf16 ? kFlush16 : kFlush32) / S::kUnit;
 
-    p.block = kCtas > 1 ? 0.37f : kTokens > 32 ? 0.27f : 0.19f;
-    p.join = 2.0f + 0.07f * static_cast<float>(plan.tokens);
-    p.part = 0.3f + 0.014f * static_cast<float>(plan.tokens);
+    // ns of a k block, of adding a tile's parts up, and of each part
+    p.cost = run_cost(Kb * (kCtas > 1 ? 370 : kTokens > 32 ? 270 : 190), 2000 + 70 * plan.tokens, 300 + 14 * plan.tokens,
+                      p.Ku);
     const void* fn = reinterpret_cast<const void*>(gemm_mx_kernel<kTokens, kCtas>);
     constexpr int kSlot = kTokens == 8 ? 100 : kTokens == 16 ? 101 : kTokens == 32 ? 102 : kTokens == 64 ? 103 : 104;
     if (S::kSmem > dev.smem_optin) return cudaErrorNotSupported;
