@@ -391,9 +391,11 @@ q4_status q4_dequant_mx(const uint8_t* codes, const uint8_t* scales, void* w_out
  * the call neither copies nor synchronizes; experts without rows cost
  * nothing.  E <= Q4_MAX_EXPERTS.
  *
- * Both use the caller's workspace (16-byte aligned, any contents, q4_gemm_mx_
- * workspace / q4_gemm_experts_workspace bytes; -1 for bad sizes, 0 where none
- * is needed, at few tokens, and NULL will do) for x's parts and partial sums.
+ * Both use the caller's workspace (16-byte aligned, any contents, at least
+ * q4_gemm_mx_workspace / q4_gemm_experts_workspace bytes) for x's parts and
+ * partial sums.  These sizes never fall as M or T grows, the matrices being the
+ * same: a workspace made for the largest batch serves all smaller ones.  0: none
+ * is needed, at few tokens, and NULL will do; -1: bad sizes.
  * It must not be used by anything else until the call has
  * run on the stream: calls that may overlap, recorded graphs among them, need
  * workspaces of their own.  Two launches a call, one at few tokens, which may

@@ -505,12 +505,14 @@ def _scratch(workspace, need: int, of: torch.Tensor, what: str):
 
 
 def q4_gemm_mx_workspace(M: int, N: int, K: int) -> int:
-    """Bytes of workspace that q4_gemm_mx needs (0: none, -1: it refuses the sizes)."""
+    """Bytes of workspace that q4_gemm_mx needs for M tokens or fewer (0: none,
+    -1: it refuses the sizes)."""
     return int(load().q4_gemm_mx_workspace(int(M), int(N), int(K)))
 
 
 def q4_gemm_experts_workspace(T: int, E: int, N: int, K: int) -> int:
-    """Bytes of workspace that q4_gemm_experts needs (0: none, -1: it refuses the sizes)."""
+    """Bytes of workspace that q4_gemm_experts needs for T rows or fewer (0: none,
+    -1: it refuses the sizes)."""
     return int(load().q4_gemm_experts_workspace(int(T), int(E), int(N), int(K)))
 
 

@@ -60,7 +60,8 @@ cudaError_t launch_pack_mx(const void* w, int type, uint8_t* codes, uint8_t* sca
 cudaError_t launch_dequant_mx(const uint8_t* codes, const uint8_t* scales, void* w, int type, int64_t E,
                               int64_t N, int64_t K, cudaStream_t s);
 // offsets == nullptr: one matrix (E = 1), T rows of x in order.
-// -1: more k blocks of output tiles than 2^31 - 1.  0: none is needed.
+// -1: more k blocks of output tiles than 2^31 - 1.  0: none is needed.  Else
+// the most that T rows or fewer need: it never falls as T grows.
 int64_t gemm_mx_workspace(int64_t T, int64_t E, int64_t N, int64_t K);
 cudaError_t launch_gemm_mx(const uint8_t* codes, const uint8_t* scales, const uint16_t* x,
                            const int32_t* rows, const int32_t* offsets, void* y, int y_type, int64_t Mx,

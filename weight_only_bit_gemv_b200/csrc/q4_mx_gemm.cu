@@ -810,6 +810,17 @@ cudaError_t launch_as(const Plan& plan, const uint8_t* codes, const uint8_t* sca
 struct DecodePlan {
     int split, groups;
 };
+constexpr int kDecodeSplits[3] = {1, 2, 4};
+constexpr int kDecodeGroups[3] = {148, 74, 33};  // clusters that run at once, of 148 SMs in one, two and four
+constexpr double kTurnStages = 0.5, kShareStages = 5.0, kAboveStages = 21.0, kAboveStages16 = 30.0;
+
+// Stages that `turns` turns take with `split` CTAs a tile, and that the kernel
+// above takes for `tiles` of its tiles.
+static double decode_stages(double turns, int64_t Ku, int split) {
+    return turns * (static_cast<double>((Ku + split - 1) / split) + kTurnStages) + (split == 1 ? 0.0 : kShareStages);
+}
+static double above_stages(double tiles, int64_t Ku, double fixed) { return tiles * static_cast<double>(Ku) / 148 + fixed; }
+
 static DecodePlan decode_plan(int64_t T, int64_t E, int64_t N, int64_t K, const Plan& plan) {
     DecodePlan best{0, 0};
     const int64_t share = (T + E - 1) / E;
@@ -818,25 +829,67 @@ static DecodePlan decode_plan(int64_t T, int64_t E, int64_t N, int64_t K, const 
     const int64_t tiles = workspace_layout(T, E, N, K, {8, false}).tiles * Nb;  // of 8 tokens
     const int64_t above = E > 1 ? tiles : Nb;                                    // the kernel above's
     const double stage = share > 4 ? 1.35 : 1.0;
-    double least = static_cast<double>(above) * Ku / 148 + (share > 8 ? 30.0 : 21.0);
-    for (int split = 1; split <= 4; split *= 2) {
-        const int most = split == 1 ? 148 : split == 2 ? 74 : 33;  // groups that run at once
+    double least = above_stages(static_cast<double>(above), Ku, share > 8 ? kAboveStages16 : kAboveStages);
+    for (int i = 0; i < 3; ++i) {
+        const int most = kDecodeGroups[i];
         const int64_t turns = (tiles + most - 1) / most;
-        const double cost = (turns * ((Ku + split - 1) / split + 0.5) + (split == 1 ? 0.0 : 5.0)) * stage;
+        const double cost = decode_stages(static_cast<double>(turns), Ku, kDecodeSplits[i]) * stage;
         if (cost < least) {
             least = cost;
-            best = {split, static_cast<int>(std::min<int64_t>(tiles, most))};
+            best = {kDecodeSplits[i], static_cast<int>(std::min<int64_t>(tiles, most))};
         }
     }
     return best;
 }
 
-int64_t gemm_mx_workspace(int64_t T, int64_t E, int64_t N, int64_t K) {
+// Whether every batch of E > 1 experts that makes lo .. hi token tiles of 8 runs
+// on q4_mx_decode.cu.  Costs are straight lines in the tiles but for the whole
+// turns, which the line through their upper ends bounds: one split that wins
+// at both ends of a range wins in all of it.  (May say no where yes holds.)
+static bool all_decode(int64_t lo, int64_t hi, int64_t Nb, int64_t Ku) {
+    for (int i = 0; i < 3; ++i) {
+        bool wins = true;
+        for (const int64_t t : {lo, hi}) {
+            const int64_t tiles = t * Nb, most = kDecodeGroups[i];
+            const double turns = lo == hi ? static_cast<double>((tiles + most - 1) / most)
+                                          : static_cast<double>(tiles - 1) / static_cast<double>(most) + 1.0;
+            wins = wins && decode_stages(turns, Ku, kDecodeSplits[i]) < above_stages(static_cast<double>(tiles), Ku, kAboveStages);
+        }
+        if (wins) return true;
+    }
+    if (lo == hi) return false;
+    const int64_t mid = lo + (hi - lo) / 2;
+    return all_decode(lo, mid, Nb, Ku) && all_decode(mid + 1, hi, Nb, Ku);
+}
+
+// Bytes that the call itself uses: 0 none, -1 too many units.
+static int64_t workspace_used(int64_t T, int64_t E, int64_t N, int64_t K) {
     const Plan plan = plan_for(T, E);
     const Workspace l = workspace_layout(T, E, N, K, plan);
     if (l.tiles > INT32_MAX / (mx_blocks(N) * mx_blocks(K))) return -1;
     if (decode_plan(T, E, N, K, plan).split > 0) return 0;
     return static_cast<int64_t>(l.bytes);
+}
+
+// The most that T rows or fewer use, so that a workspace made for the largest
+// batch serves every smaller one.  Within a class of tile sizes the bytes grow
+// with T, so the last T of each class below are all there is to compare.
+int64_t gemm_mx_workspace(int64_t T, int64_t E, int64_t N, int64_t K) {
+    int64_t most = workspace_used(T, E, N, K);
+    if (most < 0) return most;
+    if (E == 1) {
+        // one token tile of up to 64 (the decode kernel's rule changes at 4, 8 and 16), then of up to 120 each
+        for (const int64_t last : {int64_t{4}, int64_t{8}, int64_t{16}, int64_t{64}, (T - 1) / kPairTokens * kPairTokens})
+            if (last > 0 && last < T) most = std::max(most, workspace_used(last, E, N, K));
+        return most;
+    }
+    for (const int64_t share : {2, 8, 16, 64})
+        if (share * E < T) most = std::max(most, workspace_used(share * E, E, N, K));
+    const int64_t few = std::min(T, 2 * E);  // rows of which some batches run on the decode kernel
+    const Workspace l = workspace_layout(few, E, N, K, plan_for(few, E));
+    if (static_cast<int64_t>(l.bytes) > most && !all_decode(1, l.tiles, mx_blocks(N), (mx_blocks(K) + 1) / 2))
+        most = static_cast<int64_t>(l.bytes);
+    return most;
 }
 
 cudaError_t launch_gemm_mx(const uint8_t* codes, const uint8_t* scales, const uint16_t* x, const int32_t* rows,
