@@ -22,7 +22,8 @@ The microscaled 4-bit calls (q4_pack_mx and the products on it) take blocks of
 128 rows x 128 k, padded with zeros, Nb = ceil(N / 128), Kb = ceil(K / 128):
   codes    uint8              [Nb, Kb, 128, 64]   a stack of experts: [E, Nb, Kb, 128, 64]
   scales   uint8              [Nb, Kb, 512]                          [E, Nb, Kb, 512]
-They run on the tensors' device whatever the current device is, and what they
+They run on the tensors' device whatever the current device is (a stream of
+another device is refused), and what they
 allocate belongs to the stream that they run on.
 """
 from __future__ import annotations
@@ -368,6 +369,8 @@ class _Foreign:
         if stream is not None:
             if not hasattr(stream, "cuda_stream"):
                 stream = torch.cuda.ExternalStream(int(stream), device=torch.device("cuda", index))
+            elif stream.device.index != index:
+                raise ValueError(f"stream is on {stream.device}, the tensors are on cuda:{index}")
             self._guards.append(torch.cuda.stream(stream))
 
     def __enter__(self):
