@@ -387,7 +387,7 @@ q4_status q4_dequant_mx(const uint8_t* codes, const uint8_t* scales, void* w_out
  * offsets[e + 1], p < T.  offsets [E + 1] starts at 0 and does not decrease
  * (values out of order are clamped); rows of y at and past offsets[E] are set
  * to zero.  rows == NULL takes row p of x itself; a row index outside
- * [0, Mx) gives a row of zeros.  offsets and rows are read on the device, so
+ * [0, Mx) gives a row of zeros (Mx may be 0, and x then NULL).  offsets and rows are read on the device, so
  * the call neither copies nor synchronizes; experts without rows cost
  * nothing.  E <= Q4_MAX_EXPERTS.
  *

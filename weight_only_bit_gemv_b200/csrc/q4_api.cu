@@ -583,7 +583,7 @@ static q4_status run_gemm_mx(const uint8_t* codes, const uint8_t* scales, const 
     if (grouped && !rows && Mx != T) return Q4_ERR_SHAPE;
     const int64_t need = gemm_mx_workspace(T, E, N, K);
     if (need < 0) return Q4_ERR_SHAPE;
-    if (!codes || !scales || !x || !y || (need > 0 && !workspace) || (grouped && !offsets)) return Q4_ERR_NULL;
+    if (!codes || !scales || (!x && Mx > 0) || !y || (need > 0 && !workspace) || (grouped && !offsets)) return Q4_ERR_NULL;
     if ((reinterpret_cast<uintptr_t>(codes) & 31u) || !aligned16(scales) || !aligned16(x) || !aligned16(rows) ||
         !aligned16(offsets) || !aligned16(y) || !aligned16(workspace))
         return Q4_ERR_ALIGN;
