@@ -335,6 +335,12 @@ q4_status q4_gemv2(const uint8_t* codes, const uint16_t* scales,
  *                                      2 j + 1 in the high nibble of byte j
  *   scales  uint8_t [Nb][Kb][512]      row r, group g of a block at
  *                                      (r % 32) * 16 + (r / 32) * 4 + g
+ * This order is the library's own.  A matrix in the order in which microscaled
+ * checkpoints are published, row-major codes rc [N][K/2] (even k in the low
+ * nibble) and exponent bytes rs [N][ceil(K/32)], is brought into it by padding
+ * both with zeros to whole blocks and moving bytes, without a change of values:
+ *   codes[nb][kb][r][j] = rc[128 nb + r][64 kb + j]
+ *   scales[nb][kb][(r % 32) * 16 + (r / 32) * 4 + g] = rs[128 nb + r][4 kb + g]
  * A stack of E matrices (experts) is E of these in a row.  N >= 0, 1 <= K <=
  * Q4_MAX_K, any values (no multiple is asked for), and E * Nb * Kb at most
  * Q4_MX_MAX_BLOCKS; arrays of other types are row-major and contiguous.
