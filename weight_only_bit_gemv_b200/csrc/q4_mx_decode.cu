@@ -15,9 +15,10 @@
 // Clusters take the tiles in turn.  With kSplit = 1 a CTA takes whole tiles.
 // Roles: warp 0 streams codes and exponents, warp 1 issues the MMAs, warps 2-5
 // read the accumulators and write y, warps 6-10 prepare x.
-// Measured on B200 at one token: 4096 x 4096 5.8 us, of which 3 us are launch,
-// prologue, first load and epilogue; 28672 x 4096 14.4 us (4.3 TB/s; an SM
-// takes a stage of 17 KB in 0.31 us); 128256 x 4096 44.7 us (6.3 TB/s).
+// Measured on B200 at one token, back to back in a graph: 4096 x 4096 6.1 us, of
+// which 3 us are launch, prologue, first load and epilogue; 28672 x 4096 15.0 us
+// (4.2 TB/s; an SM takes a stage of 17 KB in 0.31 us); 28672 x 8192 24.9 us (5.0
+// TB/s); 128256 x 4096 44.7 us (6.3 TB/s).
 // Every wait is bounded, as in q4_mx_gemm.cu.
 #include <algorithm>
 

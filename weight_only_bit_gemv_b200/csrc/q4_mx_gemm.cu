@@ -54,9 +54,10 @@
 //
 // Measured on B200: 13 tokens x 128256 x 4096 52 us (5.5 TB/s; six exponent
 // copies and eight MMAs a stage take three quarters of its time), 64 tokens x
-// 57344 x 8192 68 us (3.9 TB/s; MMAs and copies), 512 tokens 347 us to
-// bfloat16 and 358 us to binary32 (1.39 and 1.34 PFLOP/s of 1.64; three copies
-// to every four MMAs, 14 % of the time, and waits for stages).
+// 57344 x 8192 70 us (3.8 TB/s; MMAs and copies), 512 tokens 349 us to
+// bfloat16 and 360 us to binary32 in short runs (1.38 and 1.34 PFLOP/s of 1.64;
+// three copies to every four MMAs, 14 % of the time, and waits for stages), 410
+// to 460 us once the power cap has lowered the clock.
 // Every wait is bounded; one that runs out sets an error bit and the CTA
 // drains its copies, frees its tensor memory and exits.
 #include <algorithm>
@@ -807,6 +808,8 @@ cudaError_t launch_as(const Plan& plan, const uint8_t* codes, const uint8_t* sca
 //   4096 x 4096   8.0  6.8  5.8;  9.5     28672 x 4096  14.9 16.1 14.4; 17.7
 //   4096 x 14336 21.0 13.5 10.0; 12.1     28672 x 8192  26.0 27.6 24.4; 26.6
 //   128256 x 4096 44.7 46.0 47.3; 49.6    28672 x 8192, 8 tokens 32.2 33.6 31.6; 27.0
+// The least of every row is taken but for 28672 x 4096, which the rule gives to
+// one CTA a tile (14.9 us): its three differ by less than the rule resolves.
 struct DecodePlan {
     int split, groups;
 };
